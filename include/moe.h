@@ -448,6 +448,72 @@ int moe_layer_forward_ex(const void* x, const float* w_router, const float* bias
                          int32_t* slot_out, int32_t* counts_out, void* ws, size_t ws_bytes,
                          void* stream);
 
+/* ---- 4-bit expert weights with group scales ----
+ * Post-training quantization of the experts to 4 bits (inferensys.com "Expert
+ * Parallelism" glossary, quantization entry), weights only: activations stay
+ * bf16.  `group` (32, 64 or 128) consecutive rows k of one weight column n
+ * share a scale:
+ *   s = bf16(max |v| / 7)   (1 where that is 0),
+ *   u = 8 + rne(v / s)      in 1..15;  the code u stands for (u - 8) * s.
+ * A group that holds a NaN or an infinity gets a non-finite scale and codes
+ * u = 8, so all of it reads back as NaN.  The kernels accept any code 0..15
+ * and any bf16 scale.
+ *   codes  q u8 [E, N/64, K/64, 2048]: a weight tile of 64 columns x 64 rows is
+ *          4 blocks of 16 columns of 512 bytes; a block is 32 lanes
+ *          (lane = 4 g + c) of four little-endian 32-bit words (word s: rows
+ *          16 s .. 16 s + 15); nibble i + 4 h of a word (i = 0..3, h = 0..1) is
+ *          the code of column g + 8 (i & 1), row 16 s + 8 (i >> 1) + 2 c + h.
+ *          This is the order in which a lane of the tensor-core kernel consumes
+ *          them: one 16-byte load gives a lane its operands for 64 rows.
+ *   scales bf16 [E, ceil(K/group), N] (the last group may be shorter).
+ * E K N/2 bytes of codes, 2 E ceil(K/group) N of scales. */
+
+/* Quantize bf16 weights w [E,K,N] (N contiguous).  1 <= E <= 65535, K and N
+ * multiples of 64 up to 2^20, E K N < 2^40; group 32, 64 or 128
+ * (MOE_ERR_UNSUPPORTED for other widths and groups).  Pointers 16-byte
+ * aligned.  A one-time preprocessing step. */
+int moe_quantize_weights_w4(const void* w, int64_t E, int64_t K, int64_t N, int64_t group,
+                            uint8_t* q, void* scale, void* stream);
+
+/* The values the codes stand for, rounded to bf16: w [E,K,N] =
+ * bf16((u - 8) * s).  For the layers that take bf16 weights (a long prompt
+ * through moe_layer_forward).  Shapes and errors as moe_quantize_weights_w4. */
+int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, int64_t K,
+                              int64_t N, int64_t group, void* w, void* stream);
+
+/* ---- The layer for a few tokens (a decode step) ----
+ * The whole layer for up to MOE_FEW_MAX_TOKENS tokens.  Same arguments as moe_layer_forward_ex and the
+ * same result, with two differences in rounding: the logits are accumulated
+ * in fp64 and rounded once, and h is not rounded to bf16; a token's terms are
+ * added in j order as there.  Results are bit-reproducible from run to run.  T >
+ * MOE_FEW_MAX_TOKENS, d or f not a multiple of 64: MOE_ERR_UNSUPPORTED.  x,
+ * w_router, the expert weights, y and ws 16-byte aligned.  The int32 at the
+ * start of ws is the device status word.  Two calls that may run at the same
+ * time (two streams, two graphs) need a workspace each. */
+#define MOE_FEW_MAX_TOKENS 32
+
+/* Device workspace bytes of the two calls below (0 on invalid shapes). */
+size_t moe_workspace_size_few(int64_t T, int64_t d, int64_t E, int64_t k, int64_t f);
+
+int moe_layer_forward_few(const void* x, const float* w_router, const float* bias,
+                          const void* w_gate, const void* w_up, const void* w_down, int64_t T,
+                          int64_t d, int64_t E, int64_t k, int64_t f, double cf, void* y,
+                          float* logits_out, int32_t* topk_idx_out, float* topk_w_out,
+                          int32_t* slot_out, int32_t* counts_out, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* moe_layer_forward_few on 4-bit experts: codes q_* and scales s_* from
+ * moe_quantize_weights_w4 (gate and up: K = d, N = f; down: K = f, N = d), all
+ * with the same `group`.  The products are taken on the codes, exact in bf16,
+ * and each group's fp32 sum is multiplied by its scale. */
+int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
+                             const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,
+                             const void* s_up, const uint8_t* q_down, const void* s_down,
+                             int64_t T, int64_t d, int64_t E, int64_t k, int64_t f, double cf,
+                             int64_t group, void* y, float* logits_out, int32_t* topk_idx_out,
+                             float* topk_w_out, int32_t* slot_out, int32_t* counts_out, void* ws,
+                             size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

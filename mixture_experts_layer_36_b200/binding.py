@@ -35,7 +35,12 @@ EXPORTED = ["moe_status_string", "moe_version", "moe_selftest_bounded_wait", "mo
             "moe_workspace_size_fp8", "moe_layer_forward_fp8", "moe_padded_rows",
             "moe_permute_padded", "moe_permute_fused", "moe_expert_gate_up_gather",
             "moe_expert_down_scatter", "moe_combine_finalize", "moe_workspace_size_fused",
-            "moe_layer_forward_fused", "moe_expert_mlp_buckets", "moe_layer_forward_ex"]
+            "moe_layer_forward_fused", "moe_expert_mlp_buckets", "moe_layer_forward_ex",
+            "moe_quantize_weights_w4", "moe_dequantize_weights_w4", "moe_workspace_size_few",
+            "moe_layer_forward_few", "moe_layer_forward_few_w4"]
+
+# the most tokens moe_layer_forward_few and moe_layer_forward_few_w4 take
+MOE_FEW_MAX_TOKENS = 32
 
 
 class MoEError(RuntimeError):
@@ -100,6 +105,13 @@ def _load():
                                               sz, p, p]),
         "moe_layer_forward_fp8": (ctypes.c_int, [p, p, p, p, p, p, p, p, p, i64, i64, i64, i64, i64,
                                                  dbl, p, p, sz, p]),
+        "moe_quantize_weights_w4": (ctypes.c_int, [p, i64, i64, i64, i64, p, p, p]),
+        "moe_dequantize_weights_w4": (ctypes.c_int, [p, p, i64, i64, i64, i64, p, p]),
+        "moe_workspace_size_few": (sz, [i64, i64, i64, i64, i64]),
+        "moe_layer_forward_few": (ctypes.c_int, [p, p, p, p, p, p, i64, i64, i64, i64, i64, dbl, p,
+                                                 p, p, p, p, p, p, sz, p]),
+        "moe_layer_forward_few_w4": (ctypes.c_int, [p, p, p, p, p, p, p, p, p, i64, i64, i64, i64,
+                                                    i64, dbl, i64, p, p, p, p, p, p, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -706,6 +718,146 @@ def moe_layer_forward_fp8(x, w_router, bias, wq_gate, s_gate, wq_up, s_up, wq_do
         _ptr(wq_down), _ptr(s_down), T, d, E, k, f, float(cf), _ptr(y), _ptr(ws), ws.numel(),
         _stream(stream)))
     return y, ws
+
+
+# ----------------------------------------------------------------- 4-bit experts
+
+def _on_device(tensors):
+    """The one device that all the (name, tensor) pairs live on; the calls
+    below run there, whatever the current device is."""
+    dev = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return dev
+
+
+def _w4_groups(K, group):
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    return -(-K // group)
+
+
+def moe_quantize_weights_w4(w, group=128, q=None, scale=None, stream=None):
+    """bf16 weights [E,K,N] -> (4-bit codes uint8 [E, N/64, K/64, 2048],
+    bf16 scales [E, ceil(K/group), N]); the layout is in include/moe.h."""
+    _want(w, "w", torch.bfloat16)
+    E, K, N = w.shape
+    groups = _w4_groups(K, group)
+    if K % 64 or N % 64 or not (E and K and N):
+        raise ValueError(f"K and N must be positive multiples of 64 and E positive, got {(E, K, N)}")
+    with torch.cuda.device(_on_device((("w", w), ("q", q), ("scale", scale)))), \
+            torch.cuda.stream(stream):
+        if q is None:
+            q = torch.empty(E, N // 64, K // 64, 2048, dtype=torch.uint8, device=w.device)
+        if scale is None:
+            scale = torch.empty(E, groups, N, dtype=torch.bfloat16, device=w.device)
+        _want(q, "q", torch.uint8, (E, N // 64, K // 64, 2048))
+        _want(scale, "scale", torch.bfloat16, (E, groups, N))
+        _check("moe_quantize_weights_w4", _lib.moe_quantize_weights_w4(
+            _ptr(w), E, K, N, group, _ptr(q), _ptr(scale), _stream()))
+    return q, scale
+
+
+def moe_dequantize_weights_w4(q, scale, group=128, w=None, stream=None):
+    """The bf16 weights [E,K,N] that codes and scales of
+    moe_quantize_weights_w4 stand for."""
+    _want(q, "q", torch.uint8)
+    if q.dim() != 4 or q.shape[3] != 2048:
+        raise ValueError(f"q: expected shape [E, N/64, K/64, 2048], got {tuple(q.shape)}")
+    E, N, K = q.shape[0], q.shape[1] * 64, q.shape[2] * 64
+    _want(scale, "scale", torch.bfloat16, (E, _w4_groups(K, group), N))
+    with torch.cuda.device(_on_device((("q", q), ("scale", scale), ("w", w)))), \
+            torch.cuda.stream(stream):
+        if w is None:
+            w = torch.empty(E, K, N, dtype=torch.bfloat16, device=q.device)
+        _want(w, "w", torch.bfloat16, (E, K, N))
+        _check("moe_dequantize_weights_w4", _lib.moe_dequantize_weights_w4(
+            _ptr(q), _ptr(scale), E, K, N, group, _ptr(w), _stream()))
+    return w
+
+
+# ----------------------------------------------------------------- a few tokens
+
+def moe_workspace_size_few(T, d, E, k, f):
+    return int(_lib.moe_workspace_size_few(T, d, E, k, f))
+
+
+def _few_call(name, x, w_router, bias, experts, k, cf, f, extra, y, logits, topk_idx, topk_w,
+              slot, counts, ws, stream):
+    """What the two few-token layers share: checks, buffers and the call."""
+    _want(x, "x", torch.bfloat16)
+    T, d = x.shape
+    _want(w_router, "w_router", torch.float32)
+    E = w_router.shape[1]
+    _want(w_router, "w_router", torch.float32, (d, E))
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,))
+    if T > MOE_FEW_MAX_TOKENS:
+        raise ValueError(f"{name} takes at most {MOE_FEW_MAX_TOKENS} tokens, got {T}")
+    outs = (("logits", logits, torch.float32, (T, E)), ("topk_idx", topk_idx, torch.int32, (T, k)),
+            ("topk_w", topk_w, torch.float32, (T, k)), ("slot", slot, torch.int32, (T, k)),
+            ("counts", counts, torch.int32, (E,)))
+    for n, t, dt, shape in outs:
+        if t is not None:
+            _want(t, n, dt, shape)
+    dev = _on_device((("x", x), ("w_router", w_router), ("bias", bias), *experts,
+                      *((n, t) for n, t, _, _ in outs), ("y", y), ("ws", ws)))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if ws is None:
+            ws = torch.empty(max(moe_workspace_size_few(T, d, E, k, f), 16), dtype=torch.uint8,
+                             device=dev)
+        _want(ws, "ws", torch.uint8)
+        y = torch.empty_like(x) if y is None else y
+        _want(y, "y", torch.bfloat16, (T, d))
+        _check(name, getattr(_lib, name)(
+            _ptr(x), _ptr(w_router), _ptr(bias), *(_ptr(t) for _, t in experts), T, d, E, k, f,
+            float(cf), *extra, _ptr(y), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(slot),
+            _ptr(counts), _ptr(ws), ws.numel(), _stream()))
+    return y, ws
+
+
+def moe_layer_forward_few(x, w_router, bias, w_gate, w_up, w_down, k, cf, y=None, logits=None,
+                          topk_idx=None, topk_w=None, slot=None, counts=None, ws=None,
+                          stream=None):
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens.
+    Arguments as moe_layer_forward_ex; returns (y, ws).  Keep ws (of
+    moe_workspace_size_few bytes) for the next call in a decode loop."""
+    if w_gate.dim() != 3:
+        raise ValueError(f"w_gate: expected shape [E, d, f], got {tuple(w_gate.shape)}")
+    E, d, f = w_gate.shape
+    _want(w_gate, "w_gate", torch.bfloat16, (w_router.shape[1], x.shape[1], f))
+    _want(w_up, "w_up", torch.bfloat16, (E, d, f))
+    _want(w_down, "w_down", torch.bfloat16, (E, f, d))
+    return _few_call("moe_layer_forward_few", x, w_router, bias,
+                     (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)), k, cf, f, (), y,
+                     logits, topk_idx, topk_w, slot, counts, ws, stream)
+
+
+def moe_layer_forward_few_w4(x, w_router, bias, q_gate, s_gate, q_up, s_up, q_down, s_down, k, cf,
+                             group=128, y=None, logits=None, topk_idx=None, topk_w=None, slot=None,
+                             counts=None, ws=None, stream=None):
+    """moe_layer_forward_few on 4-bit experts (codes and scales from
+    moe_quantize_weights_w4, one group size).  Returns (y, ws)."""
+    if q_gate.dim() != 4:
+        raise ValueError(f"q_gate: expected shape [E, f/64, d/64, 2048], got {tuple(q_gate.shape)}")
+    E, d, f = w_router.shape[1], x.shape[1], q_gate.shape[1] * 64
+    gd, gf = _w4_groups(d, group), _w4_groups(f, group)
+    for n, t, shape in (("q_gate", q_gate, (E, f // 64, d // 64, 2048)),
+                        ("q_up", q_up, (E, f // 64, d // 64, 2048)),
+                        ("q_down", q_down, (E, d // 64, f // 64, 2048))):
+        _want(t, n, torch.uint8, shape)
+    for n, t, shape in (("s_gate", s_gate, (E, gd, f)), ("s_up", s_up, (E, gd, f)),
+                        ("s_down", s_down, (E, gf, d))):
+        _want(t, n, torch.bfloat16, shape)
+    return _few_call("moe_layer_forward_few_w4", x, w_router, bias,
+                     (("q_gate", q_gate), ("s_gate", s_gate), ("q_up", q_up), ("s_up", s_up),
+                      ("q_down", q_down), ("s_down", s_down)), k, cf, f, (group,), y, logits,
+                     topk_idx, topk_w, slot, counts, ws, stream)
 
 
 def workspace_view(ws, field, T, d, E, k, f, cf):

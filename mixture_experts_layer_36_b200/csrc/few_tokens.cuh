@@ -1,0 +1,78 @@
+// Arguments of the few-token layer, shared by its kernel and its C entry points.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+// One expert matrix [E, K, N]: bf16 (group 0), or 4-bit codes with scales.
+struct FewMatrix {
+  const void* w;
+  const __nv_bfloat16* scale;
+  int K, N, group;
+};
+
+struct FewArgs {
+  const __nv_bfloat16* x;       // [T, d]
+  const float* w_router;        // [d, E]
+  const float* bias;            // [E] or null
+  FewMatrix gate, up, down;
+  int T, d, E, k, f, C;         // C: capacity (at most T)
+  __nv_bfloat16* y;             // [T, d]
+  float* logits;                // [T, E]
+  int32_t* topk_idx;            // [T, k]
+  float* topk_w;                // [T, k]
+  int32_t* slot;                // [T, k]
+  int32_t* counts;              // [E]
+  int32_t* status;
+  float* h;                     // [T*k, f]
+};
+
+inline size_t few_align(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Workspace header: the status word (256 bytes), then the routing results that
+// the caller did not take into buffers of its own.
+inline size_t few_header_bytes(int64_t T, int64_t E, int64_t k) {
+  return 256 + few_align(size_t(T * E) * 4) + 3 * few_align(size_t(T * k) * 4) +
+         few_align(size_t(E) * 4);
+}
+inline void few_place_header(FewArgs* a, void* ws) {
+  char* p = static_cast<char*>(ws);
+  a->status = reinterpret_cast<int32_t*>(p);
+  p += 256;
+  auto place = [&](auto*& out, size_t bytes) {
+    using P = std::remove_reference_t<decltype(out)>;
+    if (!out) out = reinterpret_cast<P>(p);
+    p += few_align(bytes);
+  };
+  place(a->logits, size_t(a->T) * a->E * 4);
+  place(a->topk_idx, size_t(a->T) * a->k * 4);
+  place(a->topk_w, size_t(a->T) * a->k * 4);
+  place(a->slot, size_t(a->T) * a->k * 4);
+  place(a->counts, size_t(a->E) * 4);
+}
+
+// The order of the selection as an unsigned integer: larger logit, larger key;
+// -0 equals +0; any NaN above every number (as a NaN token's experts have to
+// be some k distinct ones).
+__device__ __forceinline__ uint32_t few_order(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// silu in fp32 to within a few ulp (the fast intrinsics' 2^-21 would show next
+// to an h that is not rounded)
+__device__ __forceinline__ float few_silu(float z) { return z / (1.0f + expf(-z)); }
+
+size_t few_workspace_bytes(int64_t T, int64_t d, int64_t E, int64_t k, int64_t f);
+cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed);
+cudaError_t launch_quantize_w4(const __nv_bfloat16* w, int E, int K, int N, int G, uint8_t* q,
+                               __nv_bfloat16* scale, cudaStream_t s);
+cudaError_t launch_dequantize_w4(const uint8_t* q, const __nv_bfloat16* scale, int E, int K, int N,
+                                 int G, __nv_bfloat16* w, cudaStream_t s);
+
+}  // namespace moe
