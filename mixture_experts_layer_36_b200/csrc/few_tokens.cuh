@@ -28,32 +28,13 @@ struct FewArgs {
   int32_t* slot;                // [T, k]
   int32_t* counts;              // [E]
   int32_t* status;
-  float* h;                     // [T*k, f]
+  uint32_t* sync;               // grid-wide counters (few_tokens.cu)
+  double* rpart;                // router partial sums
+  float* gpart;                 // gate/up partial tiles
+  float* dpart;                 // down partial tiles
+  __nv_bfloat16* h;             // [T*k, 2, f]: h as two bf16 terms
+  int CW, CG, KS;               // router split: columns a block, column groups, row splits
 };
-
-inline size_t few_align(size_t v) { return (v + 255) & ~size_t(255); }
-
-// Workspace header: the status word (256 bytes), then the routing results that
-// the caller did not take into buffers of its own.
-inline size_t few_header_bytes(int64_t T, int64_t E, int64_t k) {
-  return 256 + few_align(size_t(T * E) * 4) + 3 * few_align(size_t(T * k) * 4) +
-         few_align(size_t(E) * 4);
-}
-inline void few_place_header(FewArgs* a, void* ws) {
-  char* p = static_cast<char*>(ws);
-  a->status = reinterpret_cast<int32_t*>(p);
-  p += 256;
-  auto place = [&](auto*& out, size_t bytes) {
-    using P = std::remove_reference_t<decltype(out)>;
-    if (!out) out = reinterpret_cast<P>(p);
-    p += few_align(bytes);
-  };
-  place(a->logits, size_t(a->T) * a->E * 4);
-  place(a->topk_idx, size_t(a->T) * a->k * 4);
-  place(a->topk_w, size_t(a->T) * a->k * 4);
-  place(a->slot, size_t(a->T) * a->k * 4);
-  place(a->counts, size_t(a->E) * 4);
-}
 
 // The order of the selection as an unsigned integer: larger logit, larger key;
 // -0 equals +0; any NaN above every number (as a NaN token's experts have to
