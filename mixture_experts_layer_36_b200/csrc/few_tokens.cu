@@ -17,9 +17,8 @@
 //      warp that arrives last adds them in CTA order, so no sum depends on
 //      timing.  h = silu(g) u is stored as two bf16 terms (hi + lo: 2^-16);
 //   D  down: the same over (expert, 256 columns of d, KB rows of f); its first
-//      weights are in flight before the last CTA has finished G.  The warp
-//      that completes a column tile of all experts adds the k weighted rows of
-//      each token in j order and writes y.
+//      weights are in flight before the last CTA has finished G.  When all are
+//      done, the k weighted rows of each token are added in j order.
 //
 // The products run on mma.sync (m16n8k16) with the weights as the 16-row
 // operand and the tokens as the 8 columns: an SM gets 23 bytes of weights a
@@ -36,18 +35,21 @@
 
 namespace moe {
 
-constexpr int kFewWarps = 8;                       // consumer warps
-constexpr int kFewThreads = 32 * kFewWarps + 32;   // and the producer warp
+constexpr int kColWarps = 8;                       // 16 columns of each half tile a warp
+constexpr int kFewWarps = 2 * kColWarps;           // consumers: one a 16-column strip
+constexpr int kWorkers = 32 * kFewWarps;
+constexpr int kFewThreads = kWorkers + 32;         // and the producer warp
 constexpr int kFewMaxCtas = 256;                   // sizes the workspace
 constexpr int kFewMaxPairs = MOE_FEW_MAX_TOKENS * 8;
-constexpr int kFewRouterRows = 512;                // router rows staged at once
+constexpr int kFewRouterRows = 384;                // router rows staged at once
 constexpr int kFewMaxSplits = 32;
 
 // grid-wide counters, zeroed by the call: arrivals of the router's partial
-// sums, of the tokens' routing and of the CTAs that finished G; then for each
-// cut gate/up tile (by the CTA that holds its first piece) and for each down
-// column tile, per warp, the blocks that are summed.
-constexpr int kSyncRouter = 0, kSyncRouted = 32, kSyncH = 64, kSyncTiles = 96;
+// sums, of the tokens' routing, of the CTAs that finished G and D; then for
+// each cut gate/up tile (by the CTA that holds its first piece), per column
+// warp, the blocks that are summed.
+constexpr int kSyncRouter = 0, kSyncRouted = 32, kSyncH = 64, kSyncY = 96, kSyncTiles = 128;
+constexpr int kSyncWords = kSyncTiles + kColWarps * kFewMaxCtas;
 
 // KIND 0: bf16; 1: codes with groups of 64 or 128 rows; 2: groups of 32.
 template <int KIND, int NBT>
@@ -60,13 +62,14 @@ struct FewCfg {
   static constexpr int kRows = 16 * NBT;                  // D: hi and lo of 8 NBT tokens
   static constexpr int kStageBytes =
       (kWBytes + kScaleBytes + kRows * kPitch + 1023) / 1024 * 1024;
-  static constexpr int kFit = 215040 / kStageBytes;
+  static constexpr int kMergeBytes = kColWarps * 32 * 16; // gate and up sums meet here
+  static constexpr int kFit = (224256 - kMergeBytes) / kStageBytes;
   static constexpr int kStages = kFit > 9 ? 9 : kFit;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kMergeBytes + 1024;
   // the router's staging uses the same memory: x (fp64), then W rows
   static constexpr int kXsBytes = 8 * NBT * kFewRouterRows * 8;
   static_assert(kXsBytes + kFewRouterRows * 32 * 4 <= kStages * kStageBytes, "router staging");
-  static_assert(256 * 8 * NBT * 8 <= kStages * kStageBytes, "router reduction");
+  static_assert(kWorkers * 8 * NBT * 8 <= kStages * kStageBytes, "router reduction");
 };
 
 struct FewShared {
@@ -125,7 +128,11 @@ __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
 __device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+}
+// the two warps that hold gate and up of the same columns
+__device__ __forceinline__ void pair_sync(int col_warp) {
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + col_warp) : "memory");
 }
 
 // Wait until the counter reaches `target`; false after kWaitLimitNs, or when
@@ -154,9 +161,14 @@ struct Line {
     if (total < parts) parts = (int)total;
   }
   __device__ long long begin(int b) const { return b < parts ? total * b / parts : total; }
-  // the piece that holds block i
+  // the piece that holds block i: the last b with begin(b) <= i, which is
+  // total * b < (i + 1) * parts; the quotient in fp32 is at most 1 off
   __device__ int piece(long long i) const {
-    return (int)(((i + 1) * parts + total - 1) / total) - 1;
+    const long long lim = (i + 1) * parts;
+    int b = (int)((float)lim / (float)total);
+    while (b > 0 && total * b >= lim) --b;
+    while (total * (b + 1) < lim) ++b;
+    return b;
   }
 };
 // A walk over one piece, block by block.
@@ -172,6 +184,18 @@ struct Walk {
     }
   }
   __device__ bool more() const { return i < end; }
+  // over `n` blocks of one unit
+  __device__ void skip(const Line& l, int n) {
+    i += n;
+    kb += n;
+    if (kb == l.nkb) {
+      kb = 0;
+      if (++c == l.nct) {
+        c = 0;
+        ++a;
+      }
+    }
+  }
   __device__ void next(const Line& l) {
     ++i;
     if (++kb == l.nkb) {
@@ -197,9 +221,9 @@ template <int NBT>
 __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
   constexpr int RR = kFewRouterRows;
   const int tid = threadIdx.x;
-  const bool worker = tid < 256;
+  const bool worker = tid < kWorkers;
   const int cg = blockIdx.x % p.CG, ks = blockIdx.x / p.CG;
-  const int c = tid % p.CW, rg = tid / p.CW, nrg = 256 / p.CW;
+  const int c = tid % p.CW, rg = tid / p.CW, nrg = kWorkers / p.CW;
   const int col0 = cg * p.CW, cols = min(p.CW, p.E - col0);
   const int k0 = (int)((long long)p.d * ks / p.KS), k1 = (int)((long long)p.d * (ks + 1) / p.KS);
   double* xs = reinterpret_cast<double*>(smem);                    // [T][RR]
@@ -214,17 +238,17 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
       const float* src = p.w_router + (size_t)base * p.E + col0;
       if (p.E % 4 == 0) {
         const int q = p.CW / 4;
-        for (int i = tid; i < len * q; i += 256) {
+        for (int i = tid; i < len * q; i += kWorkers) {
           const int r = i / q, v = i % q;
           if (4 * v < cols) cp_async16(smem_u32(wsm + r * p.CW + 4 * v), src + (size_t)r * p.E + 4 * v);
         }
       } else {
-        for (int i = tid; i < len * p.CW; i += 256) {
+        for (int i = tid; i < len * p.CW; i += kWorkers) {
           const int r = i / p.CW, v = i % p.CW;
           if (v < cols) cp_async4(smem_u32(wsm + r * p.CW + v), src + (size_t)r * p.E + v);
         }
       }
-      for (int i = tid; i < p.T * RR; i += 256) {
+      for (int i = tid; i < p.T * RR; i += kWorkers) {
         const int t = i / RR, r = i % RR;
         if (r < len) xs[i] = (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]);
       }
@@ -241,19 +265,19 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
     }
   }
   __syncthreads();
-  double* red = reinterpret_cast<double*>(smem);                   // [T][256]
+  double* red = reinterpret_cast<double*>(smem);                   // [T][kWorkers]
   if (worker) {
 #pragma unroll
     for (int t = 0; t < 8 * NBT; ++t)
-      if (t < p.T) red[t * 256 + tid] = acc[t];
+      if (t < p.T) red[t * kWorkers + tid] = acc[t];
   }
   __syncthreads();
   if (worker) {
-    for (int i = tid; i < p.T * p.CW; i += 256) {
+    for (int i = tid; i < p.T * p.CW; i += kWorkers) {
       const int t = i / p.CW, cc = i % p.CW;
       if (cc >= cols) continue;
       double s = 0.0;
-      for (int g = 0; g < nrg; ++g) s += red[t * 256 + g * p.CW + cc];
+      for (int g = 0; g < nrg; ++g) s += red[t * kWorkers + g * p.CW + cc];
       p.rpart[((size_t)ks * p.T + t) * p.E + col0 + cc] = s;
     }
   }
@@ -371,66 +395,82 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
 }
 
 // ---------------------------------------------------------------- producer
-// One stage of a block: the weights of `boxes` 64-column groups and (tokens)
-// the token rows.  Returns after issuing; `what` 1: weights, 2: token rows.
+// Fills stages with blocks of one phase.  unit() computes once for a tile what
+// its blocks share, one copy (two token rows) a lane; the block index only
+// moves the addresses.
 template <int KIND, int NBT, bool DOWN>
-__device__ __forceinline__ void few_fill(const FewArgs& p, const FewShared& sh,
-                                         const CUtensorMap* tm0, const CUtensorMap* tm1,
-                                         uint8_t* stage, uint64_t* bar, int a, int c, int kb,
-                                         int what) {
+struct Filler {
   using Cfg = FewCfg<KIND, NBT>;
-  const int lane = threadIdx.x % 32;
-  const int K = DOWN ? p.f : p.d, N = DOWN ? p.d : p.f;
-  const int klen = min(Cfg::KB, K - kb * Cfg::KB);
-  const int n = sh.row0[a + 1] - sh.row0[a];
-  const int rows = DOWN ? 2 * n : n;
-  const int e = sh.expert[a];
-  const int group = p.gate.group;
-  // 64-column groups of this tile: per matrix in G, of the one matrix in D
-  const int boxes = min(DOWN ? 4 : 2, N / 64 - c * (DOWN ? 4 : 2));
-  const int mats = DOWN ? 1 : 2;
-  const int grows = KIND == 0 ? 0 : (klen + group - 1) / group;
-  if (what & 1) {
-    if (lane == 0) {
-      const uint32_t wbytes = KIND == 0 ? 8192u : 32u * klen;
-      mbar_arrive_expect_tx(bar, mats * boxes * (wbytes + grows * 128u) + rows * klen * 2u);
+  static constexpr int kTile = DOWN ? 4 : 2;    // 64-column groups of a full tile, per matrix
+  const CUtensorMap* map;
+  const uint8_t* code;
+  const __nv_bfloat16* scale;
+  const __nv_bfloat16 *row_a, *row_b;
+  int K, lg, lane, jobs, mats, boxes, rows, e, dst, col, sdst, sjob;
+  size_t scale_step;                            // scales from one block to the next
+
+  __device__ Filler(const FewArgs& p)
+      : K(DOWN ? p.f : p.d), lg(p.lg), lane(threadIdx.x % 32),
+        mats(DOWN ? 1 : 2), scale_step((size_t)(KIND ? (Cfg::KB >> lg) : 0) * (DOWN ? p.d : p.f)) {}
+
+  __device__ void unit(const FewArgs& p, const FewShared& sh, const CUtensorMap* tm0,
+                       const CUtensorMap* tm1, int a, int c) {
+    const int N = DOWN ? p.d : p.f;
+    const int n = sh.row0[a + 1] - sh.row0[a];
+    rows = DOWN ? 2 * n : n;
+    e = sh.expert[a];
+    boxes = min(kTile, N / 64 - c * kTile);
+    jobs = mats * boxes;
+    const int m = DOWN ? 0 : (lane >= boxes);
+    const int b = lane - (m ? boxes : 0);
+    col = (c * kTile + b) * 64;
+    if constexpr (KIND == 0) {
+      map = m ? tm1 : tm0;
+      dst = (2 * m + b) * 8192;
+    } else {
+      const FewMatrix& w = DOWN ? p.down : (m ? p.up : p.gate);
+      dst = (2 * m + b) * 4096;
+      if (lane < jobs)
+        code = static_cast<const uint8_t*>(w.w) +
+               ((size_t)e * (N / 64) + c * kTile + b) * (K / 64) * 2048;
+      // scale rows: a lane's matrix and group of the block (at most 2 x 4)
+      const int per = Cfg::KB >> lg;
+      const int sm = DOWN ? 0 : (lane >= per);
+      const int sg = lane - (sm ? per : 0);
+      const FewMatrix& sw = DOWN ? p.down : (sm ? p.up : p.gate);
+      const int groups = (K + (1 << lg) - 1) >> lg;
+      sjob = lane < mats * per ? sg : 1 << 20;
+      sdst = Cfg::kWBytes + sg * 512 + sm * 256;
+      scale = sw.scale + ((size_t)e * groups + sg) * N + c * (kTile * 64);
     }
+    auto row = [&](int i) {
+      return DOWN ? p.h + (size_t)(2 * sh.row0[a] + i) * p.f
+                  : p.x + (size_t)sh.row_tok[sh.row0[a] + i] * p.d;
+    };
+    if (lane < rows) row_a = row(lane);
+    if (lane + 32 < rows) row_b = row(lane + 32);
+  }
+  __device__ void weights(uint8_t* stage, uint64_t* bar, int kb) const {
+    const int klen = min(Cfg::KB, K - kb * Cfg::KB);
+    const int grows = KIND ? (klen + (1 << lg) - 1) >> lg : 0;
+    const uint32_t wbytes = KIND == 0 ? 8192u : 32u * klen;
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar, jobs * (wbytes + grows * 128u) + rows * klen * 2u);
     __syncwarp();
     if constexpr (KIND == 0) {
-      if (lane < mats * boxes) {
-        const int m = lane / boxes, b = lane % boxes;
-        tma_load_3d(stage + (2 * m + b) * 8192, m ? tm1 : tm0, bar,
-                    (c * (DOWN ? 4 : 2) + b) * 64, kb * 64, e);
-      }
+      if (lane < jobs) tma_load_3d(stage + dst, map, bar, col, kb * 64, e);
     } else {
-      if (lane < mats * boxes) {
-        const int m = lane / boxes, b = lane % boxes;
-        const FewMatrix& w = DOWN ? p.down : (m ? p.up : p.gate);
-        const size_t tile = ((size_t)e * (N / 64) + c * (DOWN ? 4 : 2) + b) * (K / 64) + kb * 2;
-        bulk_load(stage + (2 * m + b) * 4096, static_cast<const uint8_t*>(w.w) + tile * 2048,
-                  32 * klen, bar);
-      }
-      if (lane < mats * grows) {
-        const int m = lane / grows, g = lane % grows;
-        const FewMatrix& w = DOWN ? p.down : (m ? p.up : p.gate);
-        const size_t groups = (K + group - 1) / group;
-        bulk_load(stage + Cfg::kWBytes + g * 512 + m * 256,
-                  w.scale + ((size_t)e * groups + (size_t)kb * Cfg::KB / group + g) * N +
-                      c * (DOWN ? 256 : 128),
-                  boxes * 128, bar);
-      }
+      if (lane < jobs) bulk_load(stage + dst, code + (size_t)kb * 4096, wbytes, bar);
+      if (sjob < grows) bulk_load(stage + sdst, scale + kb * scale_step, boxes * 128, bar);
     }
   }
-  if (what & 2) {
-    uint8_t* rowbuf = stage + Cfg::kWBytes + Cfg::kScaleBytes;
-    for (int i = lane; i < rows; i += 32) {
-      const __nv_bfloat16* src =
-          DOWN ? p.h + (size_t)(2 * sh.row0[a] + i) * p.f
-               : p.x + (size_t)sh.row_tok[sh.row0[a] + i] * p.d;
-      bulk_load(rowbuf + i * Cfg::kPitch, src + kb * Cfg::KB, klen * 2, bar);
-    }
+  __device__ void tokens(uint8_t* stage, uint64_t* bar, int kb) const {
+    const int klen = min(Cfg::KB, K - kb * Cfg::KB);
+    uint8_t* to = stage + Cfg::kWBytes + Cfg::kScaleBytes + lane * Cfg::kPitch;
+    if (lane < rows) bulk_load(to, row_a + kb * Cfg::KB, klen * 2, bar);
+    if (lane + 32 < rows) bulk_load(to + 32 * Cfg::kPitch, row_b + kb * Cfg::KB, klen * 2, bar);
   }
-}
+};
 
 struct Ring {
   int st = 0, n = 0;
@@ -455,44 +495,51 @@ __device__ void few_producer(const FewArgs& p, FewShared& sh, uint8_t* smem,
   Ring r;
   bool ok = true;
   auto stage = [&](int s) { return smem + s * Cfg::kStageBytes; };
+  auto empty = [&] {
+    return __all_sync(0xffffffffu, mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag)) != 0;
+  };
   {
     const Line line(sh.A, (p.f + 127) / 128, (p.d + Cfg::KB - 1) / Cfg::KB);
-    for (Walk w(line, blockIdx.x); ok && w.more(); w.next(line)) {
-      ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      if (!ok) break;
-      few_fill<KIND, NBT, false>(p, sh, tmG, tmU, stage(r.st), &sh.full[r.st], w.a, w.c, w.kb, 3);
+    Filler<KIND, NBT, false> fill(p);
+    bool fresh = true;
+    for (Walk w(line, blockIdx.x); w.more(); w.next(line)) {
+      if (fresh || w.kb == 0) fill.unit(p, sh, tmG, tmU, w.a, w.c);
+      fresh = false;
+      if (!(ok = empty())) break;
+      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
+      fill.tokens(stage(r.st), &sh.full[r.st], w.kb);
       r.next(S);
     }
   }
-  {
+  if (ok) {
     const Line line(sh.A, (p.d + 255) / 256, (p.f + Cfg::KB - 1) / Cfg::KB);
+    Filler<KIND, NBT, true> fill(p);
     Walk w(line, blockIdx.x);
     Walk w0 = w;
     Ring r0 = r;
+    bool fresh = true;
     int ahead = 0;                       // stages that hold weights but no rows yet
-    for (; ok && w.more() && ahead < S; w.next(line), ++ahead) {
-      ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      if (!ok) break;
-      few_fill<KIND, NBT, true>(p, sh, tmD, nullptr, stage(r.st), &sh.full[r.st], w.a, w.c, w.kb,
-                                1);
+    for (; w.more() && ahead < S; w.next(line), ++ahead) {
+      if (fresh || w.kb == 0) fill.unit(p, sh, tmD, tmD, w.a, w.c);
+      fresh = false;
+      if (!(ok = empty())) break;
+      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
       r.next(S);
     }
-    if (ok && ahead) {
-      ok = wait_count(p.sync + kSyncH, gridDim.x, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-    }
+    if (ok && ahead)
+      ok = __all_sync(0xffffffffu, wait_count(p.sync + kSyncH, gridDim.x, abort_flag)) != 0;
     fence_proxy_async_all();             // h was written through the generic proxy
-    for (; ok && ahead; --ahead, w0.next(line), r0.next(S))
-      few_fill<KIND, NBT, true>(p, sh, tmD, nullptr, stage(r0.st), &sh.full[r0.st], w0.a, w0.c,
-                                w0.kb, 2);
+    fresh = true;
+    for (; ok && ahead; --ahead, w0.next(line), r0.next(S)) {
+      if (fresh || w0.kb == 0) fill.unit(p, sh, tmD, tmD, w0.a, w0.c);
+      fresh = false;
+      fill.tokens(stage(r0.st), &sh.full[r0.st], w0.kb);
+    }
     for (; ok && w.more(); w.next(line)) {
-      ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      if (!ok) break;
-      few_fill<KIND, NBT, true>(p, sh, tmD, nullptr, stage(r.st), &sh.full[r.st], w.a, w.c, w.kb,
-                                3);
+      if (w.kb == 0) fill.unit(p, sh, tmD, tmD, w.a, w.c);
+      if (!(ok = empty())) break;
+      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
+      fill.tokens(stage(r.st), &sh.full[r.st], w.kb);
       r.next(S);
     }
   }
@@ -511,86 +558,116 @@ __device__ void few_producer(const FewArgs& p, FewShared& sh, uint8_t* smem,
 }
 
 // ---------------------------------------------------------------- consumers
-// acc[m][j] += weights of matrix m (16 columns of this warp) times token block j
-template <int KIND, int NBT, int NB>
-__device__ __forceinline__ void few_block(const uint8_t* stage, int klen, int group, int nb,
-                                          const bool (&valid)[2], float (&acc)[2][NB][4]) {
+// acc[j] += the weights of this warp's 16 columns times token block j.  Warps
+// 0..7 hold the first half of the tile (gate), 8..15 the second (up).  NBL:
+// token blocks.
+template <int KIND, int NBT, int NBL, int NB>
+__device__ __forceinline__ void few_block(const uint8_t* stage, int klen, int lg,
+                                          float (&acc)[NB][4]) {
   using Cfg = FewCfg<KIND, NBT>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rows = smem_u32(stage + Cfg::kWBytes + Cfg::kScaleBytes) +
                         (lane % 8) * Cfg::kPitch + (lane / 8) * 16;
   if constexpr (KIND == 0) {
-    const uint32_t base = smem_u32(stage) + (warp / 4) * 8192;
     const int chunk = 2 * (warp % 4) + ((lane / 8) & 1);
+    // row k of a swizzled tile: 128 k, its 16-byte chunk c at c ^ (k % 8)
+    const uint32_t at = smem_u32(stage) + (warp / 4) * 8192 + ((lane / 16) * 8 + lane % 8) * 128 +
+                        ((chunk ^ (lane % 8)) << 4);
 #pragma unroll
     for (int s2 = 0; s2 < 2; ++s2) {
-      uint32_t b[NB][4];
+      uint32_t b[NBL][4];
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        if (j < nb) ldsm4(b[j], rows + j * 8 * Cfg::kPitch + s2 * 64);
+      for (int j = 0; j < NBL; ++j) ldsm4(b[j], rows + j * 8 * Cfg::kPitch + s2 * 64);
 #pragma unroll
-      for (int s1 = 0; s1 < 2; ++s1) {
-        const int k = (2 * s2 + s1) * 16 + (lane / 16) * 8 + lane % 8;
-        const uint32_t at = k * 128 + ((chunk ^ (k & 7)) << 4);
+      for (int s = 0; s < 2; ++s) {
+        uint32_t a[4];
+        ldsm4_trans(a, at + (2 * s2 + s) * 2048);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (!valid[m]) continue;
-          uint32_t a[4];
-          ldsm4_trans(a, base + m * 16384 + at);
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-            if (j < nb) mma_bf16(acc[m][j], a, b[j][2 * s1], b[j][2 * s1 + 1]);
-        }
+        for (int j = 0; j < NBL; ++j) mma_bf16(acc[j], a, b[j][2 * s], b[j][2 * s + 1]);
       }
     }
   } else {
-    const int subs = klen / 64;
     const uint8_t* codes = stage + (warp / 4) * 4096 + (warp % 4) * 512 + lane * 16;
     const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(stage + Cfg::kWBytes) +
                               16 * warp + lane / 4;
     const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
-    for (int sub = 0; sub < subs; ++sub) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (!valid[m]) continue;
-        const uint4 w4 = *reinterpret_cast<const uint4*>(codes + m * 8192 + sub * 2048);
-        const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
-        uint32_t a[4][4];
+    for (int sub = 0; sub < 2; ++sub) {
+      if (sub * 64 >= klen) break;
+      const uint4 w4 = *reinterpret_cast<const uint4*>(codes + sub * 2048);
+      const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
+      uint32_t a[4][4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // 0x4300 | u is the bf16 value 128 + u
-            uint32_t v = ((words[s] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-            const __nv_bfloat162 z = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
-            a[s][i] = *reinterpret_cast<const uint32_t*>(&z);
+        for (int i = 0; i < 4; ++i) {
+          // 0x4300 | u is the bf16 value 128 + u
+          uint32_t v = ((words[s] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+          const __nv_bfloat162 z = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
+          a[s][i] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+      constexpr int GS = KIND == 1 ? 4 : 2;              // k16 steps between scalings
+#pragma unroll
+      for (int g = 0; g < 4 / GS; ++g) {
+        const int grow = KIND == 1 ? (sub * 64) >> lg : 2 * sub + g;
+        const float s0 = __bfloat162float(sc[grow * 256]);
+        const float s1 = __bfloat162float(sc[grow * 256 + 8]);
+#pragma unroll
+        for (int j = 0; j < NBL; ++j) {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < GS / 2; ++h) {
+            uint32_t b[4];
+            ldsm4(b, rows + j * 8 * Cfg::kPitch + sub * 128 + (g * GS / 2 + h) * 64);
+            mma_bf16(t, a[g * GS + 2 * h], b[0], b[1]);
+            mma_bf16(t, a[g * GS + 2 * h + 1], b[2], b[3]);
           }
-        constexpr int GS = KIND == 1 ? 4 : 2;              // k16 steps between scalings
-#pragma unroll
-        for (int g = 0; g < 4 / GS; ++g) {
-          const int grow = (sub * 64 + g * 32) / group;
-          const float s0 = __bfloat162float(sc[grow * 256 + m * 128]);
-          const float s1 = __bfloat162float(sc[grow * 256 + m * 128 + 8]);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            if (j >= nb) continue;
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < GS / 2; ++h) {
-              uint32_t b[4];
-              ldsm4(b, rows + j * 8 * Cfg::kPitch + sub * 128 + (g * GS / 2 + h) * 64);
-              mma_bf16(t, a[g * GS + 2 * h], b[0], b[1]);
-              mma_bf16(t, a[g * GS + 2 * h + 1], b[2], b[3]);
-            }
-            acc[m][j][0] = fmaf(s0, t[0], acc[m][j][0]);
-            acc[m][j][1] = fmaf(s0, t[1], acc[m][j][1]);
-            acc[m][j][2] = fmaf(s1, t[2], acc[m][j][2]);
-            acc[m][j][3] = fmaf(s1, t[3], acc[m][j][3]);
-          }
+          acc[j][0] = fmaf(s0, t[0], acc[j][0]);
+          acc[j][1] = fmaf(s0, t[1], acc[j][1]);
+          acc[j][2] = fmaf(s1, t[2], acc[j][2]);
+          acc[j][3] = fmaf(s1, t[3], acc[j][3]);
         }
       }
     }
   }
+}
+
+// The blocks of one unit that lie in this CTA's piece, NBL token blocks wide;
+// returns how many.  A warp whose wait gave up (ok = false) still walks all
+// units, without waiting or computing: warps of a pair meet after each.
+template <int KIND, int NBT, int NBL, int NB>
+__device__ __forceinline__ int few_unit(FewShared& sh, const uint8_t* smem, int K, int lg,
+                                        const Line& line, Walk& w, Ring& r, bool valid, bool& ok,
+                                        float (&acc)[NB][4]) {
+  using Cfg = FewCfg<KIND, NBT>;
+  const int lane = threadIdx.x % 32;
+  const int blocks = (int)min((long long)(line.nkb - w.kb), w.end - w.i);
+  int left = K - w.kb * Cfg::KB;
+  for (int i = 0; ok && i < blocks; ++i, left -= Cfg::KB) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag))) {
+      ok = false;
+      break;
+    }
+    if (valid) few_block<KIND, NBT, NBL, NB>(smem + r.st * Cfg::kStageBytes, left, lg, acc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[r.st]);
+    r.next(Cfg::kStages);
+  }
+  w.skip(line, blocks);
+  return blocks;
+}
+
+template <int KIND, int NBT, int NB>
+__device__ __forceinline__ int few_unit_n(FewShared& sh, const uint8_t* smem, int K, int lg,
+                                          const Line& line, Walk& w, Ring& r, int nb, bool valid, bool& ok,
+                                          float (&acc)[NB][4]) {
+  if constexpr (NB >= 8)
+    if (nb > 4) return few_unit<KIND, NBT, 8, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
+  if constexpr (NB >= 4)
+    if (nb > 2) return few_unit<KIND, NBT, 4, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
+  if constexpr (NB >= 2)
+    if (nb > 1) return few_unit<KIND, NBT, 2, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
+  return few_unit<KIND, NBT, 1, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
 }
 
 __device__ __forceinline__ void store_h(const FewArgs& p, int row, int col, float g, float u) {
@@ -604,51 +681,57 @@ __device__ __forceinline__ void store_h(const FewArgs& p, int row, int col, floa
 }
 
 // The end of a gate/up piece: h if the tile is whole, else partial sums, and h
-// by the warp whose piece completes the tile.
+// by the warp whose piece completes the tile.  Called by both warps of a pair;
+// the second one hands its sums (up) to the first.
 template <int NB>
-__device__ void few_gate_up_end(const FewArgs& p, const FewShared& sh, const Line& line, int a,
-                                int c, int blocks, bool valid, const float (&acc)[2][NB][4]) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+__device__ void few_gate_up_end(const FewArgs& p, const FewShared& sh, float* merge,
+                                const Line& line, int a, int c, int blocks,
+                                const float (&acc)[NB][4]) {
+  const int warp = threadIdx.x / 32 % kColWarps, lane = threadIdx.x % 32;
+  const bool up = threadIdx.x / 32 >= kColWarps;
   const int g = lane / 4, q = lane % 4;
   const int n = sh.row0[a + 1] - sh.row0[a];
   const int col = 16 * warp + g;
-  if (!valid) return;
-  if (blocks == line.nkb) {
+  const bool whole = blocks == line.nkb;
+  float* part = p.gpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T);
+  float4* slot = reinterpret_cast<float4*>(merge) + warp * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+  for (int j = 0; j < NB; ++j) {
+    if (8 * j >= n) break;
+    if (up) *slot = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    pair_sync(warp);
+    if (!up) {
+      const float4 o = *slot;
+      const float us[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int tok = 8 * j + 2 * q + (i & 1);
-        if (tok < n)
-          store_h(p, sh.row0[a] + tok, c * 128 + col + 8 * (i >> 1), acc[0][j][i], acc[1][j][i]);
-      }
-    return;
-  }
-  float* part = p.gpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T);
-#pragma unroll
-  for (int j = 0; j < NB; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 8 * j + 2 * q + (i & 1);
-      if (tok < n) {
-        __stcg(part + tok * 256 + col + 8 * (i >> 1), acc[0][j][i]);
-        __stcg(part + tok * 256 + 128 + col + 8 * (i >> 1), acc[1][j][i]);
+        const int tok = 8 * j + 2 * q + (i & 1), cc = col + 8 * (i >> 1);
+        if (tok >= n) continue;
+        if (whole) {
+          store_h(p, sh.row0[a] + tok, c * 128 + cc, acc[j][i], us[i]);
+        } else {
+          __stcg(part + tok * 256 + cc, acc[j][i]);
+          __stcg(part + tok * 256 + 128 + cc, us[i]);
+        }
       }
     }
+    pair_sync(warp);
+  }
+  if (whole || up) return;
   const long long u = (long long)a * line.nct + c;
   const int first = line.piece(u * line.nkb), last = line.piece((u + 1) * line.nkb - 1);
   __threadfence();
   __syncwarp();
   uint32_t old = 0;
-  if (lane == 0) old = atomicAdd(p.sync + kSyncTiles + first * kFewWarps + warp, (uint32_t)blocks);
+  if (lane == 0) old = atomicAdd(p.sync + kSyncTiles + first * kColWarps + warp, (uint32_t)blocks);
   old = __shfl_sync(0xffffffffu, old, 0);
   if (old + blocks != (uint32_t)line.nkb) return;
   __threadfence();
   for (int i = lane; i < 16 * n; i += 32) {
     const int tok = i / 16, cc = 16 * warp + i % 16;
+    const float* src = p.gpart + part_at(sh, a, c, line.nct, first, p.T) + tok * 256 + cc;
     float gs = 0.f, us = 0.f;
-    for (int b = first; b <= last; ++b) {
-      const float* src = p.gpart + part_at(sh, a, c, line.nct, b, p.T) + tok * 256 + cc;
+    for (int b = first; b <= last; ++b, src += (size_t)p.T * 256) {
       gs += __ldcg(src);
       us += __ldcg(src + 128);
     }
@@ -656,108 +739,112 @@ __device__ void few_gate_up_end(const FewArgs& p, const FewShared& sh, const Lin
   }
 }
 
-// y of this warp's columns of tile c (lane 0..15: matrix half 0, 16..31: half
-// 1) for all tokens: the weighted rows in j order, their pieces in CTA order.
-__device__ void few_combine(const FewArgs& p, const FewShared& sh, const Line& line, int c,
-                            bool valid) {
+// The end of a down piece: its partial sums (a token's two columns, from the
+// two terms of h, added).
+template <int NB>
+__device__ void few_down_end(const FewArgs& p, const FewShared& sh, const Line& line, int a, int c,
+                             const float (&acc)[NB][4]) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cc = (lane / 16) * 128 + 16 * warp + lane % 16;
-  for (int t = 0; t < p.T; ++t) {
-    int row = -1, first = 0, last = -1;
-    uint32_t at = 0;
-    if (lane < p.k) {
-      row = sh.pair_row[t * p.k + lane];
-      if (row >= 0) {
-        int a = 0;                          // the active expert that holds the row
-        for (int step = 128; step; step >>= 1)
-          if (a + step < sh.A && sh.row0[a + step] <= row) a += step;
-        const long long u = (long long)a * line.nct + c;
-        first = line.piece(u * line.nkb);
-        last = line.piece((u + 1) * line.nkb - 1);
-        at = (uint32_t)(part_at(sh, a, c, line.nct, first, p.T) / 256) + (row - sh.row0[a]);
-      }
-    }
-    float y = 0.f;
-    bool any = false;
-    for (int j = 0; j < p.k; ++j) {
-      if (__shfl_sync(0xffffffffu, row, j) < 0) continue;
-      any = true;
-      const int pieces = __shfl_sync(0xffffffffu, last - first, j);
-      const float* src = p.dpart + (size_t)__shfl_sync(0xffffffffu, at, j) * 256 + cc;
-      float o = 0.f;
-      if (valid)
-        for (int b = 0; b <= pieces; ++b) o += __ldcg(src + (size_t)b * p.T * 256);
-      y = fmaf(sh.pair_w[t * p.k + j], o, y);
-    }
-    if (valid) {
-      const size_t out = (size_t)t * p.d + c * 256 + cc;
-      p.y[out] = any ? __float2bfloat16(y) : p.x[out];
+  const int g = lane / 4, q = lane % 4;
+  const int n = sh.row0[a + 1] - sh.row0[a];
+  float* part = p.dpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T) + 16 * warp + g;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int tok = 4 * j + q;
+    if (tok < n) {
+      __stcg(part + tok * 256, acc[j][0] + acc[j][1]);
+      __stcg(part + tok * 256 + 8, acc[j][2] + acc[j][3]);
     }
   }
 }
 
-// The end of a down piece: its partial sums (a token's two columns, from the
-// two terms of h, added), and y by the warp that completes the column tile.
-template <int NB>
-__device__ void few_down_end(const FewArgs& p, const FewShared& sh, const Line& line, int a, int c,
-                             int blocks, const bool (&valid)[2], const float (&acc)[2][NB][4]) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = lane / 4, q = lane % 4;
-  const int n = sh.row0[a + 1] - sh.row0[a];
-  if (!valid[0]) return;                 // half 1 is valid only if half 0 is
-  float* part = p.dpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T);
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int tok = 4 * j + q;
-      if (tok < n && valid[m]) {
-        __stcg(part + tok * 256 + m * 128 + 16 * warp + g, acc[m][j][0] + acc[m][j][1]);
-        __stcg(part + tok * 256 + m * 128 + 16 * warp + g + 8, acc[m][j][2] + acc[m][j][3]);
-      }
+// y of 128 columns (half m of tile c, 4 a lane) of token t by one warp: the
+// weighted rows in j order, the pieces of each in CTA order.
+__device__ void few_combine(const FewArgs& p, const FewShared& sh, const Line& line, int t, int c,
+                            int m) {
+  const int lane = threadIdx.x % 32;
+  const int col = c * 256 + m * 128 + 4 * lane;
+  int pieces = -1;
+  uint32_t at = 0;
+  if (lane < p.k) {
+    const int row = sh.pair_row[t * p.k + lane];
+    if (row >= 0) {
+      int a = 0;                          // the active expert that holds the row
+      for (int step = 128; step; step >>= 1)
+        if (a + step < sh.A && sh.row0[a + step] <= row) a += step;
+      const long long u = (long long)a * line.nct + c;
+      const int first = line.piece(u * line.nkb);
+      pieces = line.piece((u + 1) * line.nkb - 1) - first;
+      at = (uint32_t)(part_at(sh, a, c, line.nct, first, p.T) / 256) + (row - sh.row0[a]);
     }
+  }
+  const bool valid = col < p.d;
+  float4 v[8];
+  int extra[8];
+  const float* src[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    extra[j] = __shfl_sync(0xffffffffu, pieces, j);
+    src[j] = p.dpart + (size_t)__shfl_sync(0xffffffffu, at, j) * 256 + m * 128 + 4 * lane;
+    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (extra[j] >= 0 && valid) v[j] = __ldcg(reinterpret_cast<const float4*>(src[j]));
+  }
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (extra[j] < 0) continue;
+    any = true;
+    for (int b = 1; b <= extra[j] && valid; ++b) {
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(src[j] + (size_t)b * p.T * 256));
+      v[j].x += o.x;
+      v[j].y += o.y;
+      v[j].z += o.z;
+      v[j].w += o.w;
+    }
+    const float w = sh.pair_w[t * p.k + j];
+    y.x = fmaf(w, v[j].x, y.x);
+    y.y = fmaf(w, v[j].y, y.y);
+    y.z = fmaf(w, v[j].z, y.z);
+    y.w = fmaf(w, v[j].w, y.w);
+  }
+  if (!valid) return;
+  const size_t out = (size_t)t * p.d + col;
+  *reinterpret_cast<uint2*>(p.y + out) =
+      any ? make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w))
+          : __ldg(reinterpret_cast<const uint2*>(p.x + out));
+}
+
+// All consumer warps of this CTA are done with a phase: its results are
+// visible, then counted.
+__device__ __forceinline__ void few_arrive(const FewShared& sh, uint32_t* counter) {
   __threadfence();
-  __syncwarp();
-  uint32_t old = 0;
-  if (lane == 0)
-    old = atomicAdd(p.sync + kSyncTiles + kFewWarps * (kFewMaxCtas + c) + warp, (uint32_t)blocks);
-  old = __shfl_sync(0xffffffffu, old, 0);
-  if (old + blocks != (uint32_t)sh.A * line.nkb) return;
-  __threadfence();
-  few_combine(p, sh, line, c, lane < 16 || valid[1]);
+  consumer_sync();
+  if (threadIdx.x == 0 && !*static_cast<const volatile int*>(&sh.abort_flag)) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+  }
 }
 
 template <int KIND, int NBT>
 __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
   using Cfg = FewCfg<KIND, NBT>;
-  constexpr int S = Cfg::kStages;
   volatile int* abort_flag = &sh.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float* merge = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes);
   Ring r;
   bool ok = true;
   {
     const Line line(sh.A, (p.f + 127) / 128, (p.d + Cfg::KB - 1) / Cfg::KB);
     Walk w(line, blockIdx.x);
-    while (ok && w.more()) {
-      float acc[2][NBT][4] = {};
+    while (w.more()) {
+      float acc[NBT][4] = {};
       const int a = w.a, c = w.c;
       const int nb = (sh.row0[a + 1] - sh.row0[a] + 7) / 8;
-      const bool v = c * 2 + warp / 4 < p.f / 64;
-      const bool valid[2] = {v, v};
-      int blocks = 0;
-      while (w.more() && w.a == a && w.c == c) {
-        ok = mbar_wait(&sh.full[r.st], r.ph, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
-        if (!ok) break;
-        few_block<KIND, NBT, NBT>(smem + r.st * Cfg::kStageBytes,
-                                  min(Cfg::KB, p.d - w.kb * Cfg::KB), p.gate.group, nb, valid, acc);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[r.st]);
-        r.next(S);
-        w.next(line);
-        ++blocks;
-      }
-      if (ok) few_gate_up_end<NBT>(p, sh, line, a, c, blocks, v, acc);
+      const bool valid = c * 2 + warp % kColWarps / 4 < p.f / 64;
+      const int blocks =
+          few_unit_n<KIND, NBT, NBT>(sh, smem, p.d, p.lg, line, w, r, nb, valid, ok, acc);
+      if (valid) few_gate_up_end<NBT>(p, sh, merge, line, a, c, ok ? blocks : 0, acc);
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -765,40 +852,35 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
     }
   }
   fence_proxy_async_all();               // h is read by asynchronous copies
-  __threadfence();
-  consumer_sync();
-  if (threadIdx.x == 0 && !*abort_flag) {
-    __threadfence();
-    atomicAdd(p.sync + kSyncH, 1u);
+  few_arrive(sh, p.sync + kSyncH);
+  const Line line(sh.A, (p.d + 255) / 256, (p.f + Cfg::KB - 1) / Cfg::KB);
+  Walk w(line, blockIdx.x);
+  while (ok && w.more()) {
+    float acc[2 * NBT][4] = {};
+    const int a = w.a, c = w.c;
+    const int nb = (2 * (sh.row0[a + 1] - sh.row0[a]) + 7) / 8;
+    const bool valid = c * 4 + warp / 4 < p.d / 64;
+    few_unit_n<KIND, NBT, 2 * NBT>(sh, smem, p.f, p.lg, line, w, r, nb, valid, ok, acc);
+    if (ok && valid) few_down_end<2 * NBT>(p, sh, line, a, c, acc);
   }
-  {
-    const Line line(sh.A, (p.d + 255) / 256, (p.f + Cfg::KB - 1) / Cfg::KB);
-    Walk w(line, blockIdx.x);
-    while (ok && w.more()) {
-      float acc[2][2 * NBT][4] = {};
-      const int a = w.a, c = w.c;
-      const int nb = (2 * (sh.row0[a + 1] - sh.row0[a]) + 7) / 8;
-      const bool valid[2] = {c * 4 + warp / 4 < p.d / 64, c * 4 + 2 + warp / 4 < p.d / 64};
-      int blocks = 0;
-      while (w.more() && w.a == a && w.c == c) {
-        ok = mbar_wait(&sh.full[r.st], r.ph, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
-        if (!ok) break;
-        few_block<KIND, NBT, 2 * NBT>(smem + r.st * Cfg::kStageBytes,
-                                      min(Cfg::KB, p.f - w.kb * Cfg::KB), p.gate.group, nb, valid,
-                                      acc);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[r.st]);
-        r.next(S);
-        w.next(line);
-        ++blocks;
-      }
-      if (ok) few_down_end<2 * NBT>(p, sh, line, a, c, blocks, valid, acc);
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      report(p.status, kDevErrWaitTimeout);
-    }
+  if (!ok && lane == 0) {
+    *abort_flag = 1;
+    report(p.status, kDevErrWaitTimeout);
+  }
+  few_arrive(sh, p.sync + kSyncY);
+
+  // ---- combine: (tile half, token) to warps, CTA by CTA
+  const int items = 2 * line.nct * p.T;
+  if ((int)blockIdx.x >= items) return;
+  if (threadIdx.x == 0) {
+    sh.ok = !*abort_flag && wait_count(p.sync + kSyncY, gridDim.x, abort_flag);
+    if (!sh.ok) report(p.status, kDevErrWaitTimeout);
+  }
+  consumer_sync();
+  if (!sh.ok) return;
+  for (int i = threadIdx.x / 32 * gridDim.x + blockIdx.x; i < items; i += kFewWarps * gridDim.x) {
+    const int t = i / (2 * line.nct), x = i - t * 2 * line.nct;
+    few_combine(p, sh, line, t, x / 2, x % 2);
   }
 }
 
@@ -854,7 +936,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 
   // ---- G and D
-  if (tid < 32 * kFewWarps)
+  if (tid < kWorkers)
     few_consumer<KIND, NBT>(p, sh, smem);
   else
     few_producer<KIND, NBT>(p, sh, smem, &tmG, &tmU, &tmD);
@@ -871,7 +953,7 @@ struct FewLayout {
   size_t sync, logits, idx, w, slot, counts, rpart, gpart, dpart, h;
   FewLayout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t f) {
     const size_t dt = (size_t)(d + 255) / 256, ft = (size_t)(f + 127) / 128;
-    sync = up256(256 + (kSyncTiles + kFewWarps * (kFewMaxCtas + dt)) * 4);
+    sync = up256(256 + kSyncWords * 4);
     logits = up256(size_t(T * E) * 4);
     idx = w = slot = up256(size_t(T * k) * 4);
     counts = up256(size_t(E) * 4);
@@ -951,6 +1033,8 @@ cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed) {
   take(a.gpart, lay.gpart);
   take(a.dpart, lay.dpart);
   take(a.h, lay.h);
+
+  a.lg = a.gate.group == 128 ? 7 : (a.gate.group == 64 ? 6 : 5);
 
   // the router's split: 32 columns (or all of a few experts') by as many row
   // ranges as there are CTAs for, at most kFewMaxSplits (a token's CTA adds them)

@@ -33,6 +33,7 @@ struct FewArgs {
   float* gpart;                 // gate/up partial tiles
   float* dpart;                 // down partial tiles
   __nv_bfloat16* h;             // [T*k, 2, f]: h as two bf16 terms
+  int lg;                       // log2 of the group (codes)
   int CW, CG, KS;               // router split: columns a block, column groups, row splits
 };
 
