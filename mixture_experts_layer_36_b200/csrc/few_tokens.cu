@@ -11,20 +11,23 @@
 //   R  router: every CTA sums its rows of x Wr in fp64 (the choice of experts
 //      must not hang on the order of a sum); the CTA of token t adds the
 //      partial sums, rounds once to fp32, and one warp picks the top k;
-//   G  gate/up: the blocks (expert, 128 columns of f, KB rows) of all chosen
-//      experts lie on one line that is cut into gridDim equal pieces.  A tile
-//      cut between CTAs goes to the workspace as fp32 partial sums, and the
-//      warp that arrives last adds them in CTA order, so no sum depends on
-//      timing.  h = silu(g) u is stored as two bf16 terms (hi + lo: 2^-16);
-//   D  down: the same over (expert, 256 columns of d, KB rows of f); its first
-//      weights are in flight before the last CTA has finished G.  When all are
-//      done, the k weighted rows of each token are added in j order.
+//   G  gate/up: units of (expert, 128 columns of f, all of d) are cut into
+//      chunks of a few blocks, which CTAs take from a counter (SMs see up to a
+//      tenth more or less of the memory's rate, so equal shares leave the fast
+//      ones idle); each chunk leaves fp32 sums in the workspace;
+//   H  the chunks of a unit are added in order and h = silu(g) u is stored for
+//      the next products (bf16 weights: as two bf16 terms, hi + lo, 2^-16);
+//   D  down: the same over (expert, 256 columns of d, all of f); its first
+//      weights are in flight while H runs;
+//   Y  the weighted sums of each token's k rows.
+// The cuts follow from the shapes and the routing alone and sums are added in
+// a fixed order, so results do not depend on which CTA took what.
 //
-// The products run on mma.sync (m16n8k16) with the weights as the 16-row
-// operand and the tokens as the 8 columns: an SM gets 23 bytes of weights a
-// clock, 12 bf16 values, which times 8 columns is a tenth of that unit's rate,
-// and the 4-bit codes become bf16 operands in registers, which tcgen05 would
-// want back in shared memory (four times the bytes the codes take there).
+// The products run on mma.sync with the weights as the 16-row operand and the
+// tokens as the 8 columns: bf16 m16n8k16 on bf16 weights, s8 m16n8k32 on codes
+// (8 clocks an SM sub-partition each).  An SM gets 23 bytes of weights a clock
+// from HBM, for which one 8-column block keeps that unit a tenth (bf16) or a
+// fifth (codes) busy; tcgen05 would want the codes back in shared memory.
 #include <type_traits>
 
 #include "abi_checks.cuh"
@@ -35,51 +38,73 @@
 
 namespace moe {
 
-constexpr int kColWarps = 8;                       // 16 columns of each half tile a warp
-constexpr int kFewWarps = 2 * kColWarps;           // consumers: one a 16-column strip
+constexpr int kFewWarps = 8;                       // consumers: two 16-column strips a warp
 constexpr int kWorkers = 32 * kFewWarps;
-constexpr int kFewThreads = kWorkers + 32;         // and the producer warp
-constexpr int kFewMaxCtas = 256;                   // sizes the workspace
+constexpr int kFewThreads = kWorkers + 64;         // and two producer warps
 constexpr int kFewMaxPairs = MOE_FEW_MAX_TOKENS * 8;
 constexpr int kFewRouterRows = 384;                // router rows staged at once
 constexpr int kFewMaxSplits = 32;
+constexpr int kFewMaxStages = 10;
+constexpr int kStripPitch = 26;
+constexpr int kDigitBytes = 3 * 144;               // 128 values of a token as int8 digits
 
-// grid-wide counters, zeroed by the call: arrivals of the router's partial
-// sums, of the tokens' routing, of the CTAs that finished G and D; then for
-// each cut gate/up tile (by the CTA that holds its first piece), per column
-// warp, the blocks that are summed.
-constexpr int kSyncRouter = 0, kSyncRouted = 32, kSyncH = 64, kSyncY = 96, kSyncTiles = 128;
-constexpr int kSyncWords = kSyncTiles + kColWarps * kFewMaxCtas;
+// A phase is cut into about kChunksPerCta chunks a CTA, of kMinChunk blocks or
+// more; sums of at most T*k*tiles + kPartRows(T) tile rows (1 KB each) are kept.
+constexpr int kChunksPerCta = 16, kMinChunk = 2;
+inline __host__ __device__ int few_part_rows(int T) { return 2560 * (T < 4 ? T : 4); }
 
-// KIND 0: bf16; 1: codes with groups of 64 or 128 rows; 2: groups of 32.
+// grid-wide counters, zeroed by the call, each on its own line: arrivals of the
+// router's partial sums, of the tokens' routing, of the CTAs that finished G,
+// H and D; the next chunk of G and of D.
+constexpr int kSyncRouter = 0, kSyncRouted = 32, kSyncG = 64, kSyncH = 96, kSyncY = 128,
+              kSyncNext = 160, kSyncWords = 224;
+
+// KIND 0: bf16; 1, 2, 3: codes with groups of 128, 64, 32 rows.
+// Tokens enter the products as bf16 rows (KIND 0: x, and h as two terms), or
+// as three rows of int8 digits (codes; few_digits below).
 template <int KIND, int NBT>
 struct FewCfg {
   static constexpr int KB = KIND == 0 ? 64 : 128;         // rows of a block
+  static constexpr int G = 256 >> KIND;                   // rows of a group (codes)
   static constexpr int kWBytes = KIND == 0 ? 32768 : 16384;
-  static constexpr int kScaleBytes = KIND == 0 ? 0 : (KIND == 1 ? 2 : 4) * 512;
-  // token rows: 16 bytes of padding keep ldmatrix free of bank conflicts
-  static constexpr int kPitch = KB * 2 + 16;
-  static constexpr int kRows = 16 * NBT;                  // D: hi and lo of 8 NBT tokens
+  static constexpr int kScaleBytes = KIND == 0 ? 0 : KB / G * 512;
+  // a token row: 128 bytes of values, 16 of padding, which keep ldmatrix free
+  // of bank conflicts (and hold the scale of the digits)
+  static constexpr int kPitch = 144;
+  static constexpr int kRows = (KIND == 0 ? 16 : 24) * NBT;
+  static constexpr int kColsG = KIND == 0 ? NBT : 3 * NBT;      // most 8-column blocks
+  static constexpr int kColsD = KIND == 0 ? 2 * NBT : 3 * NBT;
   static constexpr int kStageBytes =
       (kWBytes + kScaleBytes + kRows * kPitch + 1023) / 1024 * 1024;
-  static constexpr int kMergeBytes = kColWarps * 32 * 16; // gate and up sums meet here
-  static constexpr int kFit = (224256 - kMergeBytes) / kStageBytes;
-  static constexpr int kStages = kFit > 9 ? 9 : kFit;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kMergeBytes + 1024;
+  // codes: a warp's sums of a token's digits meet here
+  static constexpr int kStripBytes = KIND == 0 ? 0 : kFewWarps * 16 * kStripPitch * 4;
+  static constexpr int kFit = (224256 - kStripBytes) / kStageBytes;
+  static constexpr int kStages = kFit > kFewMaxStages ? kFewMaxStages : kFit;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kStripBytes + 1024;
   // the router's staging uses the same memory: x (fp64), then W rows
   static constexpr int kXsBytes = 8 * NBT * kFewRouterRows * 8;
   static_assert(kXsBytes + kFewRouterRows * 32 * 4 <= kStages * kStageBytes, "router staging");
   static_assert(kWorkers * 8 * NBT * 8 <= kStages * kStageBytes, "router reduction");
 };
 
+// What a stage holds: the first block of a chunk says which (len 0: the phase
+// is over).
+struct ChunkInfo {
+  int id, ac, kb0, len;               // ac: active expert and column tile, a << 16 | c
+};
+
 struct FewShared {
-  uint64_t full[9], empty[9];
+  uint64_t full[kFewMaxStages];       // weights, token rows and scales have landed
+  uint64_t empty[kFewMaxStages];      // all consumer warps are done with the stage
+  uint64_t ready[kFewMaxStages];      // the weights' copy is issued, info is written
+  ChunkInfo info[kFewMaxStages];
   int abort_flag, never, ok;
   uint32_t mask[256];                 // tokens that chose expert e
   uint16_t row0[257];                 // first kept row of active expert a
   uint8_t expert[256];                // active expert a -> e
   uint8_t active[256];                // e -> a
   uint8_t row_tok[kFewMaxPairs];      // kept row -> token
+  uint8_t row_a[kFewMaxPairs];        // kept row -> active expert
   int16_t pair_row[kFewMaxPairs];     // pair -> kept row, -1 dropped
   float pair_w[kFewMaxPairs];
   float logit[256];
@@ -130,9 +155,70 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
 }
-// the two warps that hold gate and up of the same columns
-__device__ __forceinline__ void pair_sync(int col_warp) {
-  asm volatile("bar.sync %0, 64;" ::"r"(2 + col_warp) : "memory");
+// c = products + (first ? init : c)
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1, bool first,
+                                       int init) {
+  if (first)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(init));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// (w & m) ^ c in one instruction
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(m), "r"(c));
+  return r;
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- digits
+// Products with 4-bit codes are taken in integers: a code is an int8 operand
+// after a mask and an xor (16 (u - 8); the bf16 operand takes four times the
+// instructions, which made that form issue-bound at 38 % of the HBM rate), and
+// s8 m16n8k32 does twice the products of bf16 m16n8k16 in the same 8 clocks.
+// 128 values of a token are held as v = rint(x 2^(22 - e)), 2^(e-1) <= max|x| <
+// 2^e, in three balanced base-256 digits: fixed point with 23 bits and sign
+// relative to the largest of the 128, exact for a bf16 x down to 2^-15 of it.
+// Every digit is a token column of the product; sums of 128 rows stay below
+// 2^21 and are exact.
+struct DigitScale {
+  float inv;        // 2^(22 - e)
+  float unit;       // 2^(e - 22) / 16, NaN if the largest is not finite
+};
+__device__ __forceinline__ DigitScale digit_scale(float mx) {
+  int e = (int)((__float_as_uint(mx) >> 23) & 255) - 126;
+  const bool bad = e > 128;
+  e = max(-100, min(e, 128));
+  DigitScale s;
+  s.inv = bad ? 0.f : __uint_as_float((uint32_t)(22 - e + 127) << 23);
+  s.unit = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(e - 26 + 127) << 23);
+  return s;
+}
+// the digits of x, lowest first, as bytes 0..2
+__device__ __forceinline__ uint32_t digits_of(float x, const DigitScale& s) {
+  const int v = s.inv == 0.f ? 0 : __float2int_rn(x * s.inv);
+  const int d0 = (int)(int8_t)(v & 255);
+  const int v1 = (v - d0) >> 8;
+  const int d1 = (int)(int8_t)(v1 & 255);
+  const int d2 = (v1 - d1) >> 8;
+  return (uint32_t)(d0 & 255) | (uint32_t)(d1 & 255) << 8 | (uint32_t)(d2 & 255) << 16;
 }
 
 // Wait until the counter reaches `target`; false after kWaitLimitNs, or when
@@ -150,70 +236,37 @@ __device__ __forceinline__ bool wait_count(const uint32_t* c, uint32_t target,
   }
 }
 
-// The blocks of a phase on one line: units (expert a, column tile c) of nkb
-// blocks each, cut into `parts` pieces of equal length (one block or more, so
-// that every piece between a unit's first and last one holds blocks of it).
-struct Line {
-  int nct, nkb, parts;
-  long long total;
-  __device__ Line(int A, int nct_, int nkb_)
-      : nct(nct_), nkb(nkb_), parts(gridDim.x), total((long long)A * nct_ * nkb_) {
-    if (total < parts) parts = (int)total;
+// The chunks of a phase.
+struct Phase {
+  int nct, nkb, len, q, chunks;       // column tiles, blocks of a unit, blocks of a chunk,
+                                      // chunks of a unit, of the phase
+  __device__ Phase(const FewShared& sh, int T, int k, int nct_, int nkb_) : nct(nct_), nkb(nkb_) {
+    const long long total = (long long)sh.A * nct * nkb;
+    const long long want = (total + gridDim.x * kChunksPerCta - 1) / (gridDim.x * kChunksPerCta);
+    len = (int)min((long long)nkb, max(want, (long long)kMinChunk));
+    q = (nkb + len - 1) / len;
+    const int rows = sh.row0[sh.A] * nct;
+    q = min(q, (T * k * nct + few_part_rows(T)) / rows);      // 1 or more: rows <= T k nct
+    len = (nkb + q - 1) / q;
+    q = (nkb + len - 1) / len;
+    chunks = sh.A * nct * q;
   }
-  __device__ long long begin(int b) const { return b < parts ? total * b / parts : total; }
-  // the piece that holds block i: the last b with begin(b) <= i, which is
-  // total * b < (i + 1) * parts; the quotient in fp32 is at most 1 off
-  __device__ int piece(long long i) const {
-    const long long lim = (i + 1) * parts;
-    int b = (int)((float)lim / (float)total);
-    while (b > 0 && total * b >= lim) --b;
-    while (total * (b + 1) < lim) ++b;
-    return b;
+  __device__ ChunkInfo info(int id) const {
+    const int u = id / q, a = u / nct;
+    ChunkInfo i;
+    i.id = id;
+    i.ac = a << 16 | (u - a * nct);
+    i.kb0 = (id - u * q) * len;
+    i.len = min(len, nkb - i.kb0);
+    return i;
   }
-};
-// A walk over one piece, block by block.
-struct Walk {
-  long long i, end;
-  int a, c, kb;
-  __device__ Walk(const Line& l, int b) : i(l.begin(b)), end(l.begin(b + 1)), a(0), c(0), kb(0) {
-    if (i < end) {
-      const long long u = i / l.nkb;
-      kb = (int)(i - u * l.nkb);
-      a = (int)(u / l.nct);
-      c = (int)(u - (long long)a * l.nct);
-    }
-  }
-  __device__ bool more() const { return i < end; }
-  // over `n` blocks of one unit
-  __device__ void skip(const Line& l, int n) {
-    i += n;
-    kb += n;
-    if (kb == l.nkb) {
-      kb = 0;
-      if (++c == l.nct) {
-        c = 0;
-        ++a;
-      }
-    }
-  }
-  __device__ void next(const Line& l) {
-    ++i;
-    if (++kb == l.nkb) {
-      kb = 0;
-      if (++c == l.nct) {
-        c = 0;
-        ++a;
-      }
-    }
+  // Float offset of the sums (256 a token) of chunk 0 of unit (a, c); the next
+  // chunk's are 256 n further.
+  __device__ size_t sums_at(const FewShared& sh, int a, int c, int n) const {
+    return 256 * (((size_t)sh.row0[a] * nct + (size_t)c * n) * q);
   }
 };
-
-// Float offset of the partial tile of unit (a, c) in CTA b: each 256 x n_a,
-// apart for every (unit, CTA) since n_a <= T.
-__device__ __forceinline__ size_t part_at(const FewShared& sh, int a, int c, int nct, int b, int T) {
-  const int n = sh.row0[a + 1] - sh.row0[a];
-  return 256 * ((size_t)sh.row0[a] * nct + (size_t)c * n + (size_t)b * T);
-}
+__device__ __forceinline__ int few_tiles(int width, int tile) { return (width + tile - 1) / tile; }
 
 // ---------------------------------------------------------------- R: router
 // Partial sums of this CTA's rows and columns for all tokens, in fp64.
@@ -283,13 +336,63 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
   }
 }
 
+// The digits of 128 values of a token, by one warp.  Row r of 16 lies at byte 4 c
+// + 2 h + v, r = 8 v + 2 c + h, the order of the codes' rows in a word: lane has
+// rows 2 c, 8 + 2 c, 2 c + 1, 9 + 2 c of 16, c = lane % 4.
+__device__ __forceinline__ void put_digits(uint8_t* out, const float (&x)[4]) {
+  const int lane = threadIdx.x % 32;
+  // as integers, |NaN| > |inf| > |finite|
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  m = __reduce_max_sync(0xffffffffu, m);
+  const DigitScale s = digit_scale(__uint_as_float(m));
+  uint32_t d[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = digits_of(x[j], s);
+#pragma unroll
+  for (int l = 0; l < 3; ++l) {
+    const uint32_t sel = 0x0040u + 0x0011u * l;              // byte l of two words
+    const uint32_t w = __byte_perm(__byte_perm(d[0], d[1], sel), __byte_perm(d[2], d[3], sel),
+                                   0x5410);
+    *reinterpret_cast<uint32_t*>(out + l * 144 + 4 * lane) = w;
+    if (lane < 4)
+      *reinterpret_cast<float*>(out + l * 144 + 128 + 4 * lane) =
+          lane == 0 ? s.unit * (float)(1 << (8 * l)) : 0.f;
+  }
+}
+
+// The digits of the tokens.
+__device__ void few_digits(const FewArgs& p) {
+  const int lane = threadIdx.x % 32, nkb = (p.d + 127) / 128;
+  if (threadIdx.x >= kWorkers) return;
+  for (int i = threadIdx.x / 32 * gridDim.x + blockIdx.x; i < p.T * nkb;
+       i += kFewWarps * gridDim.x) {
+    const int t = i / nkb, kb = i - t * nkb;
+    const int at = kb * 128 + (lane / 4) * 16 + 2 * (lane % 4);
+    uint32_t lo = 0, hi = 0;
+    if (at < p.d) {
+      const __nv_bfloat16* src = p.x + (size_t)t * p.d + at;
+      lo = __ldg(reinterpret_cast<const uint32_t*>(src));
+      hi = __ldg(reinterpret_cast<const uint32_t*>(src + 8));
+    }
+    const float x[4] = {__uint_as_float(lo << 16), __uint_as_float(hi << 16),
+                        __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi & 0xFFFF0000u)};
+    put_digits(p.xq + (size_t)i * kDigitBytes, x);
+  }
+}
+
 // Logits, top-k and gate weights of token t (all threads of one CTA).
 __device__ void few_route_token(const FewArgs& p, FewShared& sh, int t) {
   const int tid = threadIdx.x;
   if (tid < p.E) {
+    double v[kFewMaxSplits];
+#pragma unroll
+    for (int i = 0; i < kFewMaxSplits; ++i)
+      v[i] = i < p.KS ? __ldcg(p.rpart + ((size_t)i * p.T + t) * p.E + tid) : 0.0;
     double s = 0.0;
-#pragma unroll 8
-    for (int ks = 0; ks < p.KS; ++ks) s += __ldcg(p.rpart + ((size_t)ks * p.T + t) * p.E + tid);
+#pragma unroll
+    for (int i = 0; i < kFewMaxSplits; ++i) s += v[i];
     if (p.bias) s += (double)__ldg(p.bias + tid);
     const float l = (float)s;
     sh.logit[tid] = l;
@@ -388,90 +491,16 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
     const bool kept = slot < p.C;
     const int row = kept ? sh.row0[sh.active[e]] + slot : -1;
     sh.pair_row[tid] = (int16_t)row;
-    if (kept) sh.row_tok[row] = (uint8_t)t;
+    if (kept) {
+      sh.row_tok[row] = (uint8_t)t;
+      sh.row_a[row] = sh.active[e];
+    }
     if (blockIdx.x == 0) p.slot[tid] = kept ? slot : -1;
   }
   __syncthreads();
 }
 
-// ---------------------------------------------------------------- producer
-// Fills stages with blocks of one phase.  unit() computes once for a tile what
-// its blocks share, one copy (two token rows) a lane; the block index only
-// moves the addresses.
-template <int KIND, int NBT, bool DOWN>
-struct Filler {
-  using Cfg = FewCfg<KIND, NBT>;
-  static constexpr int kTile = DOWN ? 4 : 2;    // 64-column groups of a full tile, per matrix
-  const CUtensorMap* map;
-  const uint8_t* code;
-  const __nv_bfloat16* scale;
-  const __nv_bfloat16 *row_a, *row_b;
-  int K, lg, lane, jobs, mats, boxes, rows, e, dst, col, sdst, sjob;
-  size_t scale_step;                            // scales from one block to the next
-
-  __device__ Filler(const FewArgs& p)
-      : K(DOWN ? p.f : p.d), lg(p.lg), lane(threadIdx.x % 32),
-        mats(DOWN ? 1 : 2), scale_step((size_t)(KIND ? (Cfg::KB >> lg) : 0) * (DOWN ? p.d : p.f)) {}
-
-  __device__ void unit(const FewArgs& p, const FewShared& sh, const CUtensorMap* tm0,
-                       const CUtensorMap* tm1, int a, int c) {
-    const int N = DOWN ? p.d : p.f;
-    const int n = sh.row0[a + 1] - sh.row0[a];
-    rows = DOWN ? 2 * n : n;
-    e = sh.expert[a];
-    boxes = min(kTile, N / 64 - c * kTile);
-    jobs = mats * boxes;
-    const int m = DOWN ? 0 : (lane >= boxes);
-    const int b = lane - (m ? boxes : 0);
-    col = (c * kTile + b) * 64;
-    if constexpr (KIND == 0) {
-      map = m ? tm1 : tm0;
-      dst = (2 * m + b) * 8192;
-    } else {
-      const FewMatrix& w = DOWN ? p.down : (m ? p.up : p.gate);
-      dst = (2 * m + b) * 4096;
-      if (lane < jobs)
-        code = static_cast<const uint8_t*>(w.w) +
-               ((size_t)e * (N / 64) + c * kTile + b) * (K / 64) * 2048;
-      // scale rows: a lane's matrix and group of the block (at most 2 x 4)
-      const int per = Cfg::KB >> lg;
-      const int sm = DOWN ? 0 : (lane >= per);
-      const int sg = lane - (sm ? per : 0);
-      const FewMatrix& sw = DOWN ? p.down : (sm ? p.up : p.gate);
-      const int groups = (K + (1 << lg) - 1) >> lg;
-      sjob = lane < mats * per ? sg : 1 << 20;
-      sdst = Cfg::kWBytes + sg * 512 + sm * 256;
-      scale = sw.scale + ((size_t)e * groups + sg) * N + c * (kTile * 64);
-    }
-    auto row = [&](int i) {
-      return DOWN ? p.h + (size_t)(2 * sh.row0[a] + i) * p.f
-                  : p.x + (size_t)sh.row_tok[sh.row0[a] + i] * p.d;
-    };
-    if (lane < rows) row_a = row(lane);
-    if (lane + 32 < rows) row_b = row(lane + 32);
-  }
-  __device__ void weights(uint8_t* stage, uint64_t* bar, int kb) const {
-    const int klen = min(Cfg::KB, K - kb * Cfg::KB);
-    const int grows = KIND ? (klen + (1 << lg) - 1) >> lg : 0;
-    const uint32_t wbytes = KIND == 0 ? 8192u : 32u * klen;
-    if (lane == 0)
-      mbar_arrive_expect_tx(bar, jobs * (wbytes + grows * 128u) + rows * klen * 2u);
-    __syncwarp();
-    if constexpr (KIND == 0) {
-      if (lane < jobs) tma_load_3d(stage + dst, map, bar, col, kb * 64, e);
-    } else {
-      if (lane < jobs) bulk_load(stage + dst, code + (size_t)kb * 4096, wbytes, bar);
-      if (sjob < grows) bulk_load(stage + sdst, scale + kb * scale_step, boxes * 128, bar);
-    }
-  }
-  __device__ void tokens(uint8_t* stage, uint64_t* bar, int kb) const {
-    const int klen = min(Cfg::KB, K - kb * Cfg::KB);
-    uint8_t* to = stage + Cfg::kWBytes + Cfg::kScaleBytes + lane * Cfg::kPitch;
-    if (lane < rows) bulk_load(to, row_a + kb * Cfg::KB, klen * 2, bar);
-    if (lane + 32 < rows) bulk_load(to + 32 * Cfg::kPitch, row_b + kb * Cfg::KB, klen * 2, bar);
-  }
-};
-
+// ---------------------------------------------------------------- producers
 struct Ring {
   int st = 0, n = 0;
   uint32_t ph = 0;
@@ -484,86 +513,178 @@ struct Ring {
   }
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// One thread takes chunks and issues the weights' copies, one TMA box a matrix
+// and block.  It runs into phase D on its own: nothing it reads depends on G.
 template <int KIND, int NBT>
-__device__ void few_producer(const FewArgs& p, FewShared& sh, uint8_t* smem,
-                             const CUtensorMap* tmG, const CUtensorMap* tmU,
-                             const CUtensorMap* tmD) {
+__device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
+                            const CUtensorMap* tmG, const CUtensorMap* tmU,
+                            const CUtensorMap* tmD) {
   using Cfg = FewCfg<KIND, NBT>;
   constexpr int S = Cfg::kStages;
   volatile int* abort_flag = &sh.abort_flag;
-  const int lane = threadIdx.x % 32;
+  constexpr int kAt = KIND == 0 ? 64 : 4;      // box rows: 64 of bf16, 4 KB chunks of codes
   Ring r;
   bool ok = true;
-  auto stage = [&](int s) { return smem + s * Cfg::kStageBytes; };
-  auto empty = [&] {
-    return __all_sync(0xffffffffu, mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag)) != 0;
-  };
-  {
-    const Line line(sh.A, (p.f + 127) / 128, (p.d + Cfg::KB - 1) / Cfg::KB);
-    Filler<KIND, NBT, false> fill(p);
-    bool fresh = true;
-    for (Walk w(line, blockIdx.x); w.more(); w.next(line)) {
-      if (fresh || w.kb == 0) fill.unit(p, sh, tmG, tmU, w.a, w.c);
-      fresh = false;
-      if (!(ok = empty())) break;
-      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
-      fill.tokens(stage(r.st), &sh.full[r.st], w.kb);
+#pragma unroll 1
+  for (int down = 0; ok && down < 2; ++down) {
+    const Phase ph(sh, p.T, p.k, few_tiles(down ? p.d : p.f, down ? 256 : 128),
+                   few_tiles(down ? p.f : p.d, Cfg::KB));
+    uint32_t* counter = p.sync + kSyncNext + 32 * down;
+    int id = blockIdx.x;
+    while (ok && id < ph.chunks) {
+      const ChunkInfo info = ph.info(id);
+      id = gridDim.x + (int)atomicAdd(counter, 1u);          // used when this chunk is issued
+      const int e = sh.expert[info.ac >> 16], col = (info.ac & 0xFFFF) * (down ? 4 : 2);
+#pragma unroll 1
+      for (int i = 0; i < info.len; ++i) {
+        if (!(ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag))) break;
+        uint64_t* bar = &sh.full[r.st];
+        uint8_t* stage = smem + r.st * Cfg::kStageBytes;
+        if (i == 0) sh.info[r.st] = info;
+        mbar_arrive(&sh.ready[r.st]);
+        mbar_arrive_expect_tx(bar, Cfg::kWBytes);
+        const int at = (info.kb0 + i) * kAt;
+        if (down) {
+          tma_load_4d(stage, tmD, bar, 0, at, col, e);
+        } else {
+          tma_load_4d(stage, tmG, bar, 0, at, col, e);
+          tma_load_4d(stage + Cfg::kWBytes / 2, tmU, bar, 0, at, col, e);
+        }
+        r.next(S);
+      }
+    }
+    // the phase is over
+    if (ok && (ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag))) {
+      sh.info[r.st].len = 0;
+      mbar_arrive(&sh.ready[r.st]);
+      mbar_arrive(&sh.full[r.st]);
       r.next(S);
     }
   }
-  if (ok) {
-    const Line line(sh.A, (p.d + 255) / 256, (p.f + Cfg::KB - 1) / Cfg::KB);
-    Filler<KIND, NBT, true> fill(p);
-    Walk w(line, blockIdx.x);
-    Walk w0 = w;
-    Ring r0 = r;
-    bool fresh = true;
-    int ahead = 0;                       // stages that hold weights but no rows yet
-    for (; w.more() && ahead < S; w.next(line), ++ahead) {
-      if (fresh || w.kb == 0) fill.unit(p, sh, tmD, tmD, w.a, w.c);
-      fresh = false;
-      if (!(ok = empty())) break;
-      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
-      r.next(S);
-    }
-    if (ok && ahead)
-      ok = __all_sync(0xffffffffu, wait_count(p.sync + kSyncH, gridDim.x, abort_flag)) != 0;
-    fence_proxy_async_all();             // h was written through the generic proxy
-    fresh = true;
-    for (; ok && ahead; --ahead, w0.next(line), r0.next(S)) {
-      if (fresh || w0.kb == 0) fill.unit(p, sh, tmD, tmD, w0.a, w0.c);
-      fresh = false;
-      fill.tokens(stage(r0.st), &sh.full[r0.st], w0.kb);
-    }
-    for (; ok && w.more(); w.next(line)) {
-      if (w.kb == 0) fill.unit(p, sh, tmD, tmD, w.a, w.c);
-      if (!(ok = empty())) break;
-      fill.weights(stage(r.st), &sh.full[r.st], w.kb);
-      fill.tokens(stage(r.st), &sh.full[r.st], w.kb);
-      r.next(S);
-    }
-  }
-  if (!ok && lane == 0) {
+  if (!ok) {
     *abort_flag = 1;
     report(p.status, kDevErrWaitTimeout);
   }
-  __syncwarp();
   // every copy has landed before the CTA may exit
-  if (lane == 0) {
-    for (int back = 1; back <= S && back <= r.n; ++back) {
-      const int it = r.n - back;
-      if (!mbar_wait(&sh.full[it % S], (it / S) & 1, &sh.never)) break;
+  for (int back = 1; back <= S && back <= r.n; ++back) {
+    const int it = r.n - back;
+    if (!mbar_wait(&sh.full[it % S], (it / S) & 1, &sh.never)) break;
+  }
+}
+
+// One warp adds the token rows and the scales, by 16-byte cp.async of all
+// lanes: their pieces are small, and a bulk copy each took 150 clocks to issue,
+// which bound the stream at 60 % of the HBM rate.
+template <int KIND, int NBT, bool DOWN>
+__device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem, Ring& r) {
+  using Cfg = FewCfg<KIND, NBT>;
+  constexpr int kTile = DOWN ? 256 : 128;
+  constexpr int kScaleRows = KIND ? Cfg::KB / Cfg::G : 0;
+  constexpr int kStep = KIND ? kDigitBytes : 128;           // bytes of a token row's block
+  constexpr int kChunks = kStep / 16;
+  const int lane = threadIdx.x % 32;
+  const int K = DOWN ? p.f : p.d, N = DOWN ? p.d : p.f;
+  const int row_bytes = KIND ? few_tiles(K, 128) * kDigitBytes : K * 2;
+  const uint8_t* rows_at = KIND ? (DOWN ? p.hq : p.xq)
+                                : reinterpret_cast<const uint8_t*>(DOWN ? p.h : p.x);
+  bool waited = !DOWN;
+  while (true) {
+    bool ok = mbar_wait(&sh.ready[r.st], r.ph, &sh.abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const ChunkInfo info = sh.info[r.st];
+    if (info.len == 0) {
+      mbar_arrive(&sh.full[r.st]);
+      r.next(Cfg::kStages);
+      return true;
+    }
+    if (!waited) {                                          // h of all tokens is there
+      ok = wait_count(p.sync + kSyncH, gridDim.x, &sh.abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      waited = true;
+    }
+    const int a = info.ac >> 16, c = info.ac & 0xFFFF;
+    const int row0 = sh.row0[a], n = sh.row0[a + 1] - row0;
+    const int chunks = (DOWN && KIND == 0 ? 2 * n : n) * kChunks;
+    // 16 bytes i of the rows: row, and place in its block
+    auto src = [&](int i) {
+      const int t = i / kChunks, o = (i - t * kChunks) * 16;
+      const int row = DOWN ? (KIND == 0 ? 2 * row0 + t : row0 + t) : sh.row_tok[row0 + t];
+      return rows_at + (size_t)row * row_bytes + o;
+    };
+    auto dst = [&](int i) {
+      return KIND ? i * 16 : (i / kChunks) * Cfg::kPitch + (i % kChunks) * 16;
+    };
+    const uint8_t* mine = src(lane < chunks ? lane : 0) + (size_t)info.kb0 * kStep;
+    const uint32_t mine_to = Cfg::kWBytes + Cfg::kScaleBytes + dst(lane);
+    const __nv_bfloat16* scale = nullptr;
+    if constexpr (KIND != 0) {
+      // lane -> 8 columns: of the tile, or of gate (0..15) and up (16..31)
+      const int n0 = c * kTile + 8 * (DOWN ? lane : lane % 16);
+      const FewMatrix& w = DOWN ? p.down : (lane / 16 ? p.up : p.gate);
+      if (n0 < N)
+        scale = w.scale + ((size_t)sh.expert[a] * few_tiles(K, Cfg::G) +
+                           (size_t)info.kb0 * kScaleRows) * N + n0;
+    }
+#pragma unroll 1
+    for (int i = 0; i < info.len; ++i) {
+      if (i) {
+        ok = mbar_wait(&sh.ready[r.st], r.ph, &sh.abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+      }
+      const uint32_t stage = smem_u32(smem + r.st * Cfg::kStageBytes);
+      if constexpr (KIND != 0) {
+        if (scale) {
+          // rows past the last group (zero digits) take its scales
+          const int last = few_tiles(K - (info.kb0 + i) * Cfg::KB, Cfg::G) - 1;
+#pragma unroll
+          for (int g = 0; g < kScaleRows; ++g)
+            cp_async16(stage + Cfg::kWBytes + g * 512 + lane * 16,
+                       scale + (size_t)min(g, last) * N);
+          scale += (size_t)kScaleRows * N;
+        }
+      }
+      if (lane < chunks) cp_async16(stage + mine_to, mine);
+      for (int j = lane + 32; j < chunks; j += 32)
+        cp_async16(stage + Cfg::kWBytes + Cfg::kScaleBytes + dst(j),
+                   src(j) + (size_t)(info.kb0 + i) * kStep);
+      mine += kStep;
+      // this lane's arrival, when its copies have landed
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_u32(&sh.full[r.st]))
+                   : "memory");
+      r.next(Cfg::kStages);
     }
   }
 }
 
+template <int KIND, int NBT>
+__device__ void few_tokens(const FewArgs& p, FewShared& sh, uint8_t* smem) {
+  Ring r;
+  bool ok = few_tokens_phase<KIND, NBT, false>(p, sh, smem, r);
+  ok = ok && few_tokens_phase<KIND, NBT, true>(p, sh, smem, r);
+  if (!ok && threadIdx.x % 32 == 0) {
+    *static_cast<volatile int*>(&sh.abort_flag) = 1;
+    report(p.status, kDevErrWaitTimeout);
+  }
+  cp_async_wait();
+}
+
 // ---------------------------------------------------------------- consumers
-// acc[j] += the weights of this warp's 16 columns times token block j.  Warps
-// 0..7 hold the first half of the tile (gate), 8..15 the second (up).  NBL:
-// token blocks.
-template <int KIND, int NBT, int NBL, int NB>
-__device__ __forceinline__ void few_block(const uint8_t* stage, int klen, int lg,
-                                          float (&acc)[NB][4]) {
+// acc[m][j] += the weights of this warp's strip m times token block j.  A
+// warp's strips are columns 16 w .. 16 w + 15 of the tile's two halves (gate and
+// up).  NBL: token blocks.  Rows past the matrix's end hold zero weights (bf16)
+// or zero digits, columns past it give sums that nobody stores: no block needs
+// a branch (conditions on either cost a thousand bytes of register spills).
+template <int KIND, int NBT, int NBL>
+__device__ __forceinline__ void few_block(const uint8_t* stage, float (&acc)[2][NBL][4]) {
   using Cfg = FewCfg<KIND, NBT>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rows = smem_u32(stage + Cfg::kWBytes + Cfg::kScaleBytes) +
@@ -579,236 +700,279 @@ __device__ __forceinline__ void few_block(const uint8_t* stage, int klen, int lg
 #pragma unroll
       for (int j = 0; j < NBL; ++j) ldsm4(b[j], rows + j * 8 * Cfg::kPitch + s2 * 64);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t a[4];
-        ldsm4_trans(a, at + (2 * s2 + s) * 2048);
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < NBL; ++j) mma_bf16(acc[j], a, b[j][2 * s], b[j][2 * s + 1]);
-      }
+        for (int m = 0; m < 2; ++m) {
+          uint32_t a[4];
+          ldsm4_trans(a, at + m * 16384 + (2 * s2 + s) * 2048);
+#pragma unroll
+          for (int j = 0; j < NBL; ++j) mma_bf16(acc[m][j], a, b[j][2 * s], b[j][2 * s + 1]);
+        }
     }
   } else {
+    constexpr float kMagic = 12582912.f;                // 1.5 2^23: sums start as its bits
+    constexpr int kMagicBits = 0x4B400000;
+    constexpr int kGroups = Cfg::KB / Cfg::G, kPer = 4 / kGroups;    // groups; k32 steps of one
     const uint8_t* codes = stage + (warp / 4) * 4096 + (warp % 4) * 512 + lane * 16;
     const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(stage + Cfg::kWBytes) +
                               16 * warp + lane / 4;
-    const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
+    const uint8_t* unit = stage + Cfg::kWBytes + Cfg::kScaleBytes + 128 + (lane % 4) * 2 * 144;
+    // both strips' words first: their loads overlap
+    uint4 w4[2][2];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      if (sub * 64 >= klen) break;
-      const uint4 w4 = *reinterpret_cast<const uint4*>(codes + sub * 2048);
-      const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
-      uint32_t a[4][4];
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int sub = 0; sub < 2; ++sub)
+        w4[m][sub] = *reinterpret_cast<const uint4*>(codes + m * 8192 + sub * 2048);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // 0x4300 | u is the bf16 value 128 + u
-          uint32_t v = ((words[s] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-          const __nv_bfloat162 z = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
-          a[s][i] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-      constexpr int GS = KIND == 1 ? 4 : 2;              // k16 steps between scalings
+    for (int j0 = 0; j0 < NBL; j0 += 3) {                // 3 token blocks at a time
+      constexpr int NJ = NBL < 3 ? NBL : 3;
+      uint32_t b[NJ][2][4];
+      float u0[NJ], u1[NJ];
 #pragma unroll
-      for (int g = 0; g < 4 / GS; ++g) {
-        const int grow = KIND == 1 ? (sub * 64) >> lg : 2 * sub + g;
-        const float s0 = __bfloat162float(sc[grow * 256]);
-        const float s1 = __bfloat162float(sc[grow * 256 + 8]);
+      for (int j = 0; j < NJ; ++j) {
+        ldsm4(b[j][0], rows + (j0 + j) * 8 * Cfg::kPitch);
+        ldsm4(b[j][1], rows + (j0 + j) * 8 * Cfg::kPitch + 64);
+        u0[j] = *reinterpret_cast<const float*>(unit + (j0 + j) * 8 * 144);
+        u1[j] = *reinterpret_cast<const float*>(unit + (j0 + j) * 8 * 144 + 144);
+      }
 #pragma unroll
-        for (int j = 0; j < NBL; ++j) {
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int m = 0; m < 2; ++m) {
+        int t[NJ][4];
 #pragma unroll
-          for (int h = 0; h < GS / 2; ++h) {
-            uint32_t b[4];
-            ldsm4(b, rows + j * 8 * Cfg::kPitch + sub * 128 + (g * GS / 2 + h) * 64);
-            mma_bf16(t, a[g * GS + 2 * h], b[0], b[1]);
-            mma_bf16(t, a[g * GS + 2 * h + 1], b[2], b[3]);
+        for (int h = 0; h < 4; ++h) {
+          const uint4& w = w4[m][h / 2];
+          const uint32_t lo = h % 2 ? w.z : w.x, hi = h % 2 ? w.w : w.y;
+          // even nibbles: column g; odd ones: column g + 8; 16 (u - 8) as int8
+          const uint32_t a0 = and_xor(lo << 4, 0xF0F0F0F0u, 0x80808080u);
+          const uint32_t a1 = and_xor(lo, 0xF0F0F0F0u, 0x80808080u);
+          const uint32_t a2 = and_xor(hi << 4, 0xF0F0F0F0u, 0x80808080u);
+          const uint32_t a3 = and_xor(hi, 0xF0F0F0F0u, 0x80808080u);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            mma_s8(t[j], a0, a1, a2, a3, b[j][h / 2][h % 2 * 2], b[j][h / 2][h % 2 * 2 + 1],
+                   h % kPer == 0, kMagicBits);
+          // the group's integer sums, scaled, into the fp32 sums
+          if (h % kPer == kPer - 1) {
+            const int g = kGroups == 1 ? 0 : h / kPer;
+            const float s0 = __bfloat162float(sc[g * 256 + m * 128]);
+            const float s1 = __bfloat162float(sc[g * 256 + m * 128 + 8]);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              float(&c)[4] = acc[m][j0 + j];
+              c[0] = fmaf((__int_as_float(t[j][0]) - kMagic) * u0[j], s0, c[0]);
+              c[1] = fmaf((__int_as_float(t[j][1]) - kMagic) * u1[j], s0, c[1]);
+              c[2] = fmaf((__int_as_float(t[j][2]) - kMagic) * u0[j], s1, c[2]);
+              c[3] = fmaf((__int_as_float(t[j][3]) - kMagic) * u1[j], s1, c[3]);
+            }
           }
-          acc[j][0] = fmaf(s0, t[0], acc[j][0]);
-          acc[j][1] = fmaf(s0, t[1], acc[j][1]);
-          acc[j][2] = fmaf(s1, t[2], acc[j][2]);
-          acc[j][3] = fmaf(s1, t[3], acc[j][3]);
         }
       }
     }
   }
 }
 
-// The blocks of one unit that lie in this CTA's piece, NBL token blocks wide;
-// returns how many.  A warp whose wait gave up (ok = false) still walks all
-// units, without waiting or computing: warps of a pair meet after each.
-template <int KIND, int NBT, int NBL, int NB>
-__device__ __forceinline__ int few_unit(FewShared& sh, const uint8_t* smem, int K, int lg,
-                                        const Line& line, Walk& w, Ring& r, bool valid, bool& ok,
-                                        float (&acc)[NB][4]) {
+// One chunk, NBL token blocks wide: its blocks, then this warp's two strips of
+// its sums.  False when a wait gave up.
+template <int KIND, int NBT, int NBL, bool DOWN>
+__device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const uint8_t* smem,
+                                          float* strip, Ring& r, const ChunkInfo& info, int n,
+                                          float* sums) {
   using Cfg = FewCfg<KIND, NBT>;
-  const int lane = threadIdx.x % 32;
-  const int blocks = (int)min((long long)(line.nkb - w.kb), w.end - w.i);
-  int left = K - w.kb * Cfg::KB;
-  for (int i = 0; ok && i < blocks; ++i, left -= Cfg::KB) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag))) {
-      ok = false;
-      break;
-    }
-    if (valid) few_block<KIND, NBT, NBL, NB>(smem + r.st * Cfg::kStageBytes, left, lg, acc);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int c = info.ac & 0xFFFF;
+  // strips past the matrix's width have nothing to do
+  const int c64 = (DOWN ? p.d : p.f) / 64 - c * (DOWN ? 4 : 2) - warp / 4;
+  const bool valid[2] = {c64 > 0, DOWN ? c64 > 2 : c64 > 0};
+  float acc[2][NBL][4] = {};
+#pragma unroll 1
+  for (int i = 0; i < info.len; ++i) {
+    if (i && !__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag)))
+      return false;
+    few_block<KIND, NBT, NBL>(smem + r.st * Cfg::kStageBytes, acc);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[r.st]);
     r.next(Cfg::kStages);
   }
-  w.skip(line, blocks);
-  return blocks;
-}
-
-template <int KIND, int NBT, int NB>
-__device__ __forceinline__ int few_unit_n(FewShared& sh, const uint8_t* smem, int K, int lg,
-                                          const Line& line, Walk& w, Ring& r, int nb, bool valid, bool& ok,
-                                          float (&acc)[NB][4]) {
-  if constexpr (NB >= 8)
-    if (nb > 4) return few_unit<KIND, NBT, 8, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
-  if constexpr (NB >= 4)
-    if (nb > 2) return few_unit<KIND, NBT, 4, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
-  if constexpr (NB >= 2)
-    if (nb > 1) return few_unit<KIND, NBT, 2, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
-  return few_unit<KIND, NBT, 1, NB>(sh, smem, K, lg, line, w, r, valid, ok, acc);
-}
-
-__device__ __forceinline__ void store_h(const FewArgs& p, int row, int col, float g, float u) {
-  const float h = few_silu(g) * u;
-  const __nv_bfloat16 hi = __float2bfloat16(h);
-  const float hf = __bfloat162float(hi);
-  // an infinite or NaN h has no second term
-  const __nv_bfloat16 lo = __float2bfloat16(fabsf(hf) <= 3.4e38f ? h - hf : 0.f);
-  p.h[(size_t)(2 * row) * p.f + col] = hi;
-  p.h[(size_t)(2 * row + 1) * p.f + col] = lo;
-}
-
-// The end of a gate/up piece: h if the tile is whole, else partial sums, and h
-// by the warp whose piece completes the tile.  Called by both warps of a pair;
-// the second one hands its sums (up) to the first.
-template <int NB>
-__device__ void few_gate_up_end(const FewArgs& p, const FewShared& sh, float* merge,
-                                const Line& line, int a, int c, int blocks,
-                                const float (&acc)[NB][4]) {
-  const int warp = threadIdx.x / 32 % kColWarps, lane = threadIdx.x % 32;
-  const bool up = threadIdx.x / 32 >= kColWarps;
   const int g = lane / 4, q = lane % 4;
-  const int n = sh.row0[a + 1] - sh.row0[a];
-  const int col = 16 * warp + g;
-  const bool whole = blocks == line.nkb;
-  float* part = p.gpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T);
-  float4* slot = reinterpret_cast<float4*>(merge) + warp * 32 + lane;
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    if (8 * j >= n) break;
-    if (up) *slot = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-    pair_sync(warp);
-    if (!up) {
-      const float4 o = *slot;
-      const float us[4] = {o.x, o.y, o.z, o.w};
+  for (int m = 0; m < 2; ++m) {
+    if (!valid[m]) continue;
+    float* to = sums + m * 128 + 16 * warp;
+    if constexpr (KIND == 0 && !DOWN) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 8 * j + 2 * q + (i & 1), cc = col + 8 * (i >> 1);
-        if (tok >= n) continue;
-        if (whole) {
-          store_h(p, sh.row0[a] + tok, c * 128 + cc, acc[j][i], us[i]);
-        } else {
-          __stcg(part + tok * 256 + cc, acc[j][i]);
-          __stcg(part + tok * 256 + 128 + cc, us[i]);
+      for (int j = 0; j < NBL; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 8 * j + 2 * q + (i & 1);
+          if (tok < n) __stcg(to + tok * 256 + g + 8 * (i >> 1), acc[m][j][i]);
+        }
+    } else if constexpr (KIND == 0) {        // a token's two columns: the two terms of h
+#pragma unroll
+      for (int j = 0; j < NBL; ++j) {
+        const int tok = 4 * j + q;
+        if (tok < n) {
+          __stcg(to + tok * 256 + g, acc[m][j][0] + acc[m][j][1]);
+          __stcg(to + tok * 256 + g + 8, acc[m][j][2] + acc[m][j][3]);
+        }
+      }
+    } else {
+      // a token's three columns: its digits; 8 tokens at a time through the
+      // warp's strip, then lane -> (column lane % 16, token 2 i + lane / 16)
+#pragma unroll
+      for (int ch = 0; ch < (NBL + 2) / 3; ++ch) {
+        __syncwarp();
+#pragma unroll
+        for (int jj = 3 * ch; jj < NBL && jj < 3 * ch + 3; ++jj) {
+          float* put = strip + g * kStripPitch + (jj - 3 * ch) * 8 + 2 * q;
+          *reinterpret_cast<float2*>(put) = make_float2(acc[m][jj][0], acc[m][jj][1]);
+          *reinterpret_cast<float2*>(put + 8 * kStripPitch) =
+              make_float2(acc[m][jj][2], acc[m][jj][3]);
+        }
+        __syncwarp();
+        const float* get = strip + (lane % 16) * kStripPitch;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 2 * i + lane / 16;
+          if (8 * ch + t < n)
+            __stcg(to + (8 * ch + t) * 256 + lane % 16,
+                   get[3 * t + 2] + (get[3 * t + 1] + get[3 * t]));
         }
       }
     }
-    pair_sync(warp);
   }
-  if (whole || up) return;
-  const long long u = (long long)a * line.nct + c;
-  const int first = line.piece(u * line.nkb), last = line.piece((u + 1) * line.nkb - 1);
-  __threadfence();
-  __syncwarp();
-  uint32_t old = 0;
-  if (lane == 0) old = atomicAdd(p.sync + kSyncTiles + first * kColWarps + warp, (uint32_t)blocks);
-  old = __shfl_sync(0xffffffffu, old, 0);
-  if (old + blocks != (uint32_t)line.nkb) return;
-  __threadfence();
-  for (int i = lane; i < 16 * n; i += 32) {
-    const int tok = i / 16, cc = 16 * warp + i % 16;
-    const float* src = p.gpart + part_at(sh, a, c, line.nct, first, p.T) + tok * 256 + cc;
-    float gs = 0.f, us = 0.f;
-    for (int b = first; b <= last; ++b, src += (size_t)p.T * 256) {
-      gs += __ldcg(src);
-      us += __ldcg(src + 128);
+  return true;
+}
+
+// All chunks of a phase that this CTA takes.
+template <int KIND, int NBT, bool DOWN>
+__device__ __forceinline__ bool few_phase(const FewArgs& p, FewShared& sh, const uint8_t* smem,
+                                          float* strip, Ring& r, const Phase& ph) {
+  using Cfg = FewCfg<KIND, NBT>;
+  constexpr int NB = DOWN ? Cfg::kColsD : Cfg::kColsG;
+  constexpr int kPerToken = KIND ? 3 : (DOWN ? 2 : 1);
+#pragma unroll 1
+  while (true) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag))) return false;
+    const ChunkInfo info = sh.info[r.st];
+    if (info.len == 0) {
+      __syncwarp();
+      if (threadIdx.x % 32 == 0) mbar_arrive(&sh.empty[r.st]);
+      r.next(Cfg::kStages);
+      return true;
     }
-    store_h(p, sh.row0[a] + tok, c * 128 + cc, gs, us);
+    const int a = info.ac >> 16, n = sh.row0[a + 1] - sh.row0[a];
+    float* sums = p.part + ph.sums_at(sh, a, info.ac & 0xFFFF, n) +
+                  (size_t)(info.kb0 / ph.len) * n * 256;
+    const int nb = (n * kPerToken + 7) / 8;
+    bool ok;
+    // as wide as needed: 1, 2, 4, 8 blocks (bf16), 1, 2, 3, 6, 12 (digits)
+    if (nb == 1)
+      ok = few_chunk<KIND, NBT, 1, DOWN>(p, sh, smem, strip, r, info, n, sums);
+    else if (nb == 2)
+      ok = few_chunk<KIND, NBT, (NB < 2 ? 1 : 2), DOWN>(p, sh, smem, strip, r, info, n, sums);
+    else if (nb <= (KIND ? 3 : 4))
+      ok = few_chunk<KIND, NBT, (KIND ? 3 : (NB < 4 ? NB : 4)), DOWN>(p, sh, smem, strip, r, info,
+                                                                     n, sums);
+    else if (nb <= (KIND ? 6 : 8))
+      ok = few_chunk<KIND, NBT, (KIND ? (NB < 6 ? NB : 6) : NB), DOWN>(p, sh, smem, strip, r, info,
+                                                                     n, sums);
+    else
+      ok = few_chunk<KIND, NBT, NB, DOWN>(p, sh, smem, strip, r, info, n, sums);
+    if (!ok) return false;
   }
 }
 
-// The end of a down piece: its partial sums (a token's two columns, from the
-// two terms of h, added).
-template <int NB>
-__device__ void few_down_end(const FewArgs& p, const FewShared& sh, const Line& line, int a, int c,
-                             const float (&acc)[NB][4]) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = lane / 4, q = lane % 4;
-  const int n = sh.row0[a + 1] - sh.row0[a];
-  float* part = p.dpart + part_at(sh, a, c, line.nct, blockIdx.x, p.T) + 16 * warp + g;
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int tok = 4 * j + q;
-    if (tok < n) {
-      __stcg(part + tok * 256, acc[j][0] + acc[j][1]);
-      __stcg(part + tok * 256 + 8, acc[j][2] + acc[j][3]);
-    }
-  }
+// The sums of row r's unit in column tile c, from column `col` on: where they
+// start, and how far apart the chunks' are.
+struct Sums {
+  const float* at;
+  size_t step;
+};
+__device__ __forceinline__ Sums few_sums(const FewArgs& p, const FewShared& sh, const Phase& ph,
+                                         int r, int c, int col) {
+  const int a = sh.row_a[r], n = sh.row0[a + 1] - sh.row0[a];
+  return {p.part + ph.sums_at(sh, a, c, n) + (r - sh.row0[a]) * 256 + col, (size_t)n * 256};
 }
 
-// y of 128 columns (half m of tile c, 4 a lane) of token t by one warp: the
-// weighted rows in j order, the pieces of each in CTA order.
-__device__ void few_combine(const FewArgs& p, const FewShared& sh, const Line& line, int t, int c,
-                            int m) {
+// h of one row in one tile of 128 columns, by one warp: lane -> columns 2 c,
+// 2 c + 1, 8 + 2 c, 9 + 2 c of 16 (the order of the digits).
+template <int KIND>
+__device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, int row, int c) {
   const int lane = threadIdx.x % 32;
-  const int col = c * 256 + m * 128 + 4 * lane;
-  int pieces = -1;
-  uint32_t at = 0;
-  if (lane < p.k) {
-    const int row = sh.pair_row[t * p.k + lane];
-    if (row >= 0) {
-      int a = 0;                          // the active expert that holds the row
-      for (int step = 128; step; step >>= 1)
-        if (a + step < sh.A && sh.row0[a + step] <= row) a += step;
-      const long long u = (long long)a * line.nct + c;
-      const int first = line.piece(u * line.nkb);
-      pieces = line.piece((u + 1) * line.nkb - 1) - first;
-      at = (uint32_t)(part_at(sh, a, c, line.nct, first, p.T) / 256) + (row - sh.row0[a]);
+  const int at = (lane / 4) * 16 + 2 * (lane % 4);
+  const bool valid = c * 128 + at < p.f;
+  const Sums s = few_sums(p, sh, ph, row, c, at);
+  float g[4] = {}, u[4] = {};
+  if (valid) {
+#pragma unroll 8
+    for (int i = 0; i < ph.q; ++i) {
+      const float* src = s.at + i * s.step;
+      const float2 g0 = __ldcg(reinterpret_cast<const float2*>(src));
+      const float2 g1 = __ldcg(reinterpret_cast<const float2*>(src + 8));
+      const float2 u0 = __ldcg(reinterpret_cast<const float2*>(src + 128));
+      const float2 u1 = __ldcg(reinterpret_cast<const float2*>(src + 136));
+      g[0] += g0.x, g[1] += g0.y, g[2] += g1.x, g[3] += g1.y;
+      u[0] += u0.x, u[1] += u0.y, u[2] += u1.x, u[3] += u1.y;
     }
   }
-  const bool valid = col < p.d;
-  float4 v[8];
-  int extra[8];
-  const float* src[8];
+  float h[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    extra[j] = __shfl_sync(0xffffffffu, pieces, j);
-    src[j] = p.dpart + (size_t)__shfl_sync(0xffffffffu, at, j) * 256 + m * 128 + 4 * lane;
-    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (extra[j] >= 0 && valid) v[j] = __ldcg(reinterpret_cast<const float4*>(src[j]));
+  for (int i = 0; i < 4; ++i) h[i] = few_silu(g[i]) * u[i];
+  if constexpr (KIND == 0) {
+    if (!valid) return;
+    float lo[4];
+    __nv_bfloat162 hi[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = __floats2bfloat162_rn(h[2 * i], h[2 * i + 1]);
+      const float f0 = __low2float(hi[i]), f1 = __high2float(hi[i]);
+      // an infinite or NaN h has no second term
+      lo[2 * i] = fabsf(f0) <= 3.4e38f ? h[2 * i] - f0 : 0.f;
+      lo[2 * i + 1] = fabsf(f1) <= 3.4e38f ? h[2 * i + 1] - f1 : 0.f;
+    }
+    __nv_bfloat16* out = p.h + (size_t)(2 * row) * p.f + c * 128 + at;
+    *reinterpret_cast<__nv_bfloat162*>(out) = hi[0];
+    *reinterpret_cast<__nv_bfloat162*>(out + 8) = hi[1];
+    *reinterpret_cast<uint32_t*>(out + p.f) = pack_bf16x2(lo[0], lo[1]);
+    *reinterpret_cast<uint32_t*>(out + p.f + 8) = pack_bf16x2(lo[2], lo[3]);
+  } else {
+    const float x[4] = {h[0], h[2], h[1], h[3]};
+    put_digits(p.hq + ((size_t)row * ph.nct + c) * kDigitBytes, x);
   }
+}
+
+// y of 32 columns of token t by one warp: lane -> (columns 4 (lane % 8), every
+// fourth of the chunks of the token's rows, row after row); the four lanes'
+// weighted sums are added last.
+__device__ void few_combine(const FewArgs& p, const FewShared& sh, const Phase& ph, int t,
+                            int col32) {
+  const int lane = threadIdx.x % 32;
+  const int col = 32 * col32 + 4 * (lane % 8), c = col / 256;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
   bool any = false;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (extra[j] < 0) continue;
-    any = true;
-    for (int b = 1; b <= extra[j] && valid; ++b) {
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(src[j] + (size_t)b * p.T * 256));
-      v[j].x += o.x;
-      v[j].y += o.y;
-      v[j].z += o.z;
-      v[j].w += o.w;
-    }
+  for (int j = 0; j < p.k; ++j) any = any || sh.pair_row[t * p.k + j] >= 0;
+  const int terms = p.k * ph.q;
+#pragma unroll 8
+  for (int i = lane / 8; i < terms; i += 4) {
+    const int j = i / ph.q, row = sh.pair_row[t * p.k + j];
+    if (row < 0) continue;
+    const Sums s = few_sums(p, sh, ph, row, c, col % 256);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s.at + (i - j * ph.q) * s.step));
     const float w = sh.pair_w[t * p.k + j];
-    y.x = fmaf(w, v[j].x, y.x);
-    y.y = fmaf(w, v[j].y, y.y);
-    y.z = fmaf(w, v[j].z, y.z);
-    y.w = fmaf(w, v[j].w, y.w);
+    y.x = fmaf(w, v.x, y.x);
+    y.y = fmaf(w, v.y, y.y);
+    y.z = fmaf(w, v.z, y.z);
+    y.w = fmaf(w, v.w, y.w);
   }
-  if (!valid) return;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+    y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+    y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
+    y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+  }
+  if (lane >= 8) return;
   const size_t out = (size_t)t * p.d + col;
   *reinterpret_cast<uint2*>(p.y + out) =
       any ? make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w))
@@ -825,63 +989,51 @@ __device__ __forceinline__ void few_arrive(const FewShared& sh, uint32_t* counte
     atomicAdd(counter, 1u);
   }
 }
+// ... and all CTAs are.
+__device__ __forceinline__ bool few_await(FewShared& sh, const uint32_t* counter) {
+  if (threadIdx.x == 0) sh.ok = wait_count(counter, gridDim.x, &sh.abort_flag);
+  consumer_sync();
+  const bool ok = sh.ok;
+  consumer_sync();
+  return ok;
+}
 
 template <int KIND, int NBT>
 __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
   using Cfg = FewCfg<KIND, NBT>;
-  volatile int* abort_flag = &sh.abort_flag;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float* merge = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes);
+  const int warp = threadIdx.x / 32;
+  float* strip = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes) +
+                 warp * 16 * kStripPitch;
   Ring r;
-  bool ok = true;
-  {
-    const Line line(sh.A, (p.f + 127) / 128, (p.d + Cfg::KB - 1) / Cfg::KB);
-    Walk w(line, blockIdx.x);
-    while (w.more()) {
-      float acc[NBT][4] = {};
-      const int a = w.a, c = w.c;
-      const int nb = (sh.row0[a + 1] - sh.row0[a] + 7) / 8;
-      const bool valid = c * 2 + warp % kColWarps / 4 < p.f / 64;
-      const int blocks =
-          few_unit_n<KIND, NBT, NBT>(sh, smem, p.d, p.lg, line, w, r, nb, valid, ok, acc);
-      if (valid) few_gate_up_end<NBT>(p, sh, merge, line, a, c, ok ? blocks : 0, acc);
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      report(p.status, kDevErrWaitTimeout);
-    }
+  const Phase up(sh, p.T, p.k, few_tiles(p.f, 128), few_tiles(p.d, Cfg::KB));
+  bool ok = few_phase<KIND, NBT, false>(p, sh, smem, strip, r, up);
+  if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
+  few_arrive(sh, p.sync + kSyncG);
+
+  const int rows = sh.row0[sh.A];
+  if ((int)blockIdx.x < rows * up.nct) {     // (row, tile) to warps, CTA by CTA
+    ok = few_await(sh, p.sync + kSyncG) && ok;
+    if (ok)
+      for (int i = warp * gridDim.x + blockIdx.x; i < rows * up.nct; i += kFewWarps * gridDim.x)
+        few_h<KIND>(p, sh, up, i / up.nct, i % up.nct);
   }
-  fence_proxy_async_all();               // h is read by asynchronous copies
   few_arrive(sh, p.sync + kSyncH);
-  const Line line(sh.A, (p.d + 255) / 256, (p.f + Cfg::KB - 1) / Cfg::KB);
-  Walk w(line, blockIdx.x);
-  while (ok && w.more()) {
-    float acc[2 * NBT][4] = {};
-    const int a = w.a, c = w.c;
-    const int nb = (2 * (sh.row0[a + 1] - sh.row0[a]) + 7) / 8;
-    const bool valid = c * 4 + warp / 4 < p.d / 64;
-    few_unit_n<KIND, NBT, 2 * NBT>(sh, smem, p.f, p.lg, line, w, r, nb, valid, ok, acc);
-    if (ok && valid) few_down_end<2 * NBT>(p, sh, line, a, c, acc);
-  }
-  if (!ok && lane == 0) {
-    *abort_flag = 1;
-    report(p.status, kDevErrWaitTimeout);
-  }
+
+  const Phase down(sh, p.T, p.k, few_tiles(p.d, 256), few_tiles(p.f, Cfg::KB));
+  ok = ok && few_phase<KIND, NBT, true>(p, sh, smem, strip, r, down);
+  if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
   few_arrive(sh, p.sync + kSyncY);
 
-  // ---- combine: (tile half, token) to warps, CTA by CTA
-  const int items = 2 * line.nct * p.T;
-  if ((int)blockIdx.x >= items) return;
-  if (threadIdx.x == 0) {
-    sh.ok = !*abort_flag && wait_count(p.sync + kSyncY, gridDim.x, abort_flag);
-    if (!sh.ok) report(p.status, kDevErrWaitTimeout);
+  const int items = p.d / 32 * p.T;          // (token, 32 columns) to warps
+  if ((int)blockIdx.x < items) {
+    ok = few_await(sh, p.sync + kSyncY) && ok;
+    if (ok)
+      for (int i = warp * gridDim.x + blockIdx.x; i < items; i += kFewWarps * gridDim.x) {
+        const int t = i / (p.d / 32);
+        few_combine(p, sh, down, t, i - t * (p.d / 32));
+      }
   }
-  consumer_sync();
-  if (!sh.ok) return;
-  for (int i = threadIdx.x / 32 * gridDim.x + blockIdx.x; i < items; i += kFewWarps * gridDim.x) {
-    const int t = i / (2 * line.nct), x = i - t * 2 * line.nct;
-    few_combine(p, sh, line, t, x / 2, x % 2);
-  }
+  if (!ok && threadIdx.x % 32 == 0) report(p.status, kDevErrWaitTimeout);
 }
 
 template <int KIND, int NBT>
@@ -897,7 +1049,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   volatile int* abort_flag = &sh.abort_flag;
   if (tid == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
-      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.full[s], 1 + 32);        // the weights' thread, and each token lane
+      mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], kFewWarps);
     }
     sh.abort_flag = 0;
@@ -907,14 +1060,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
 
   // ---- R: router, top-k, tables
-  if ((int)blockIdx.x < p.KS * p.CG) {
-    few_router_rows<NBT>(p, smem);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) atomicAdd(p.sync + kSyncRouter, 1u);
-  }
+  if constexpr (KIND != 0) few_digits(p);
+  if ((int)blockIdx.x < p.KS * p.CG) few_router_rows<NBT>(p, smem);
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) atomicAdd(p.sync + kSyncRouter, 1u);
   if ((int)blockIdx.x < p.T) {
-    if (tid == 0) sh.ok = wait_count(p.sync + kSyncRouter, p.KS * p.CG, abort_flag);
+    if (tid == 0) sh.ok = wait_count(p.sync + kSyncRouter, gridDim.x, abort_flag);
     __syncthreads();
     if (sh.ok)
       for (int t = blockIdx.x; t < p.T; t += gridDim.x) few_route_token(p, sh, t);
@@ -924,7 +1076,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     sh.ok = wait_count(p.sync + kSyncRouted, p.T, abort_flag);
     if (!sh.ok) report(p.status, kDevErrWaitTimeout);
   }
-  fence_proxy_async_smem();              // the router's staging becomes the ring
+  fence_proxy_async_all();               // the router's staging becomes the ring
   __syncthreads();
   if (!sh.ok) return;
   few_tables(p, sh);
@@ -936,10 +1088,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 
   // ---- G and D
-  if (tid < kWorkers)
+  if (tid < kWorkers) {
     few_consumer<KIND, NBT>(p, sh, smem);
-  else
-    few_producer<KIND, NBT>(p, sh, smem, &tmG, &tmU, &tmD);
+  } else if (tid < kWorkers + 32) {
+    if (elect_one()) few_weights<KIND, NBT>(p, sh, smem, &tmG, &tmU, &tmD);
+  } else {
+    few_tokens<KIND, NBT>(p, sh, smem);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -950,7 +1105,7 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 // Byte sizes of the workspace, in order: the counters (with the status word
 // first), the routing results, then what the phases hand on.
 struct FewLayout {
-  size_t sync, logits, idx, w, slot, counts, rpart, gpart, dpart, h;
+  size_t sync, logits, idx, w, slot, counts, rpart, part, xq, h;
   FewLayout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t f) {
     const size_t dt = (size_t)(d + 255) / 256, ft = (size_t)(f + 127) / 128;
     sync = up256(256 + kSyncWords * 4);
@@ -958,14 +1113,46 @@ struct FewLayout {
     idx = w = slot = up256(size_t(T * k) * 4);
     counts = up256(size_t(E) * 4);
     rpart = up256(size_t(kFewMaxSplits * T * E) * 8);
-    gpart = (size_t(T * k) * ft + size_t(kFewMaxCtas) * T) * 1024;
-    dpart = (size_t(T * k) * dt + size_t(kFewMaxCtas) * T) * 1024;
-    h = up256(size_t(T * k * f) * 4);
+    // G's sums are read before D's are written
+    part = (size_t(T * k) * (ft > dt ? ft : dt) + few_part_rows((int)T)) * 1024;
+    xq = up256(size_t(T) * ((d + 127) / 128) * kDigitBytes);
+    // two bf16 terms, or digits
+    h = up256(size_t(T * k) * (ft * kDigitBytes > size_t(f) * 4 ? ft * kDigitBytes : size_t(f) * 4));
   }
   size_t total() const {
-    return sync + logits + idx + w + slot + counts + rpart + gpart + dpart + h;
+    return sync + logits + idx + w + slot + counts + rpart + part + xq + h;
   }
 };
+
+// One matrix as a 4-D tensor, a box being `groups` 64-column groups of one
+// block, each group's bytes together: bf16 as (64 columns, K rows, N/64 groups,
+// E), 128-byte swizzle, 64 rows a box; codes as (1 KB, 1 KB chunks of a group,
+// N/64 groups, E), 4 chunks (128 rows) a box.  Boxes that reach past K or N
+// read zeros there.
+bool map_few(CUtensorMap* m, const FewMatrix& w, uint64_t E, uint32_t groups) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const uint64_t K = w.K, N = w.N;
+  const bool codes = w.group != 0;
+  cuuint64_t dims[4] = {64, K, N / 64, E};
+  cuuint64_t strides[3] = {N * 2, 128, K * N * 2};
+  cuuint32_t box[4] = {64, 64, groups, 1};
+  if (codes) {
+    dims[0] = 256;
+    dims[1] = K / 32;
+    strides[0] = 1024;
+    strides[1] = K * 32;
+    strides[2] = K * N / 2;
+    box[0] = 256;
+    box[1] = 4;
+  }
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(w.w), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
 
 template <int KIND, int NBT>
 cudaError_t launch_few_t(const FewArgs& a, int grid, const CUtensorMap& g, const CUtensorMap& u,
@@ -1012,7 +1199,7 @@ cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed) {
   DeviceInfo* di = nullptr;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
-  const int grid = di->sms < kFewMaxCtas ? di->sms : kFewMaxCtas;
+  const int grid = di->sms;
 
   const FewLayout lay(a.T, a.d, a.E, a.k, a.f);
   char* at = static_cast<char*>(ws);
@@ -1030,11 +1217,10 @@ cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed) {
   take(a.slot, lay.slot);
   take(a.counts, lay.counts);
   take(a.rpart, lay.rpart);
-  take(a.gpart, lay.gpart);
-  take(a.dpart, lay.dpart);
-  take(a.h, lay.h);
-
-  a.lg = a.gate.group == 128 ? 7 : (a.gate.group == 64 ? 6 : 5);
+  take(a.part, lay.part);
+  take(a.xq, lay.xq);
+  a.h = reinterpret_cast<__nv_bfloat16*>(at);
+  a.hq = reinterpret_cast<uint8_t*>(at);
 
   // the router's split: 32 columns (or all of a few experts') by as many row
   // ranges as there are CTAs for, at most kFewMaxSplits (a token's CTA adds them)
@@ -1045,15 +1231,14 @@ cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed) {
   if (a.KS > kFewMaxSplits) a.KS = kFewMaxSplits;
 
   CUtensorMap g{}, u{}, dn{};
-  if (a.gate.group == 0 &&
-      (!map_weights(&g, a.gate.w, a.E, a.d, a.f) || !map_weights(&u, a.up.w, a.E, a.d, a.f) ||
-       !map_weights(&dn, a.down.w, a.E, a.f, a.d))) {
+  if (!map_few(&g, a.gate, a.E, 2) || !map_few(&u, a.up, a.E, 2) || !map_few(&dn, a.down, a.E, 4)) {
     *map_failed = true;
     return cudaSuccess;
   }
   if ((err = cudaMemsetAsync(ws, 0, lay.sync, s)) != cudaSuccess) return err;
   if (a.gate.group == 0) return launch_few_kind<0>(a, grid, g, u, dn, di, s);
-  if (a.gate.group == 32) return launch_few_kind<2>(a, grid, g, u, dn, di, s);
+  if (a.gate.group == 64) return launch_few_kind<2>(a, grid, g, u, dn, di, s);
+  if (a.gate.group == 32) return launch_few_kind<3>(a, grid, g, u, dn, di, s);
   return launch_few_kind<1>(a, grid, g, u, dn, di, s);
 }
 

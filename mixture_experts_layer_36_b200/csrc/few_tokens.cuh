@@ -30,10 +30,10 @@ struct FewArgs {
   int32_t* status;
   uint32_t* sync;               // grid-wide counters (few_tokens.cu)
   double* rpart;                // router partial sums
-  float* gpart;                 // gate/up partial tiles
-  float* dpart;                 // down partial tiles
-  __nv_bfloat16* h;             // [T*k, 2, f]: h as two bf16 terms
-  int lg;                       // log2 of the group (codes)
+  float* part;                  // sums of the chunks of G, then of D
+  uint8_t* xq;                  // codes: x as digits, [T, ceil(d/128), 3, 144]
+  uint8_t* hq;                  // codes: h as digits, [T*k, ceil(f/128), 3, 144]
+  __nv_bfloat16* h;             // bf16: [T*k, 2, f], h as two bf16 terms
   int CW, CG, KS;               // router split: columns a block, column groups, row splits
 };
 

@@ -127,12 +127,12 @@ inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 bloc
 // 14-15 CTA-pair GEMM with expert tails (its gathering instance 30)
 // (+16: the gathering instance of a grouped GEMM slot's kernel, +32: the
 // scattering one); 19-22 router GEMM with the top-k epilogue (the router
-// kernels have no gathering instance, so 3-6 + 16 is free for them); 48-56
-// the few-token layer (3 weight forms x 3 batch sizes)
+// kernels have no gathering instance, so 3-6 + 16 is free for them); 48-59
+// the few-token layer (4 weight forms x 3 batch sizes)
 constexpr int kFewAttrSlot = 48;
 struct DeviceInfo {
   int sms = 0;
-  bool attr_set[57] = {};
+  bool attr_set[60] = {};
 };
 inline DeviceInfo g_dev[64];
 
