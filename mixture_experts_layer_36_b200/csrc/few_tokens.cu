@@ -87,10 +87,10 @@ struct FewCfg {
   static_assert(kWorkers * 8 * NBT * 8 <= kStages * kStageBytes, "router reduction");
 };
 
-// What a stage holds: the first block of a chunk says which (len 0: the phase
-// is over).
-struct ChunkInfo {
-  int id, ac, kb0, len;               // ac: active expert and column tile, a << 16 | c
+// The chunk whose first block a stage holds (len 0: the phase is over).
+struct alignas(16) ChunkInfo {
+  int len, kb0, a, c;                 // blocks, the first one; active expert, column tile
+  int n, row0, e, sums;               // its rows and expert; where its sums go (1 KB each)
 };
 
 struct FewShared {
@@ -251,20 +251,22 @@ struct Phase {
     q = (nkb + len - 1) / len;
     chunks = sh.A * nct * q;
   }
-  __device__ ChunkInfo info(int id) const {
-    const int u = id / q, a = u / nct;
+  __device__ ChunkInfo info(const FewShared& sh, int id) const {
+    const int u = id / q, a = u / nct, qi = id - u * q;
     ChunkInfo i;
-    i.id = id;
-    i.ac = a << 16 | (u - a * nct);
-    i.kb0 = (id - u * q) * len;
+    i.a = a;
+    i.c = u - a * nct;
+    i.kb0 = qi * len;
     i.len = min(len, nkb - i.kb0);
+    i.row0 = sh.row0[a];
+    i.n = sh.row0[a + 1] - i.row0;
+    i.e = sh.expert[a];
+    i.sums = tile_at(i.row0, i.n, i.c) + qi * i.n;
     return i;
   }
-  // Float offset of the sums (256 a token) of chunk 0 of unit (a, c); the next
-  // chunk's are 256 n further.
-  __device__ size_t sums_at(const FewShared& sh, int a, int c, int n) const {
-    return 256 * (((size_t)sh.row0[a] * nct + (size_t)c * n) * q);
-  }
+  // Where the sums of chunk 0 of a unit lie, in tokens of 256 floats (1 KB); the
+  // next chunk's are n further.
+  __device__ int tile_at(int row0, int n, int c) const { return (row0 * nct + c * n) * q; }
 };
 __device__ __forceinline__ int few_tiles(int width, int tile) { return (width + tile - 1) / tile; }
 
@@ -272,18 +274,18 @@ __device__ __forceinline__ int few_tiles(int width, int tile) { return (width + 
 // Partial sums of this CTA's rows and columns for all tokens, in fp64.
 template <int NBT>
 __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
-  constexpr int RR = kFewRouterRows;
+  constexpr int RR = kFewRouterRows, TT = 8 * NBT;
   const int tid = threadIdx.x;
   const bool worker = tid < kWorkers;
   const int cg = blockIdx.x % p.CG, ks = blockIdx.x / p.CG;
   const int c = tid % p.CW, rg = tid / p.CW, nrg = kWorkers / p.CW;
   const int col0 = cg * p.CW, cols = min(p.CW, p.E - col0);
   const int k0 = (int)((long long)p.d * ks / p.KS), k1 = (int)((long long)p.d * (ks + 1) / p.KS);
-  double* xs = reinterpret_cast<double*>(smem);                    // [T][RR]
-  float* wsm = reinterpret_cast<float*>(smem + 8 * NBT * RR * 8);  // [RR][CW]
-  double acc[8 * NBT];
+  double* xs = reinterpret_cast<double*>(smem);                    // [RR][TT]
+  float* wsm = reinterpret_cast<float*>(smem + TT * RR * 8);       // [RR][CW]
+  double acc[TT];
 #pragma unroll
-  for (int t = 0; t < 8 * NBT; ++t) acc[t] = 0.0;
+  for (int t = 0; t < TT; ++t) acc[t] = 0.0;
   for (int base = k0; base < k1; base += RR) {
     const int len = min(RR, k1 - base);
     if (base != k0) __syncthreads();
@@ -293,7 +295,8 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
         const int q = p.CW / 4;
         for (int i = tid; i < len * q; i += kWorkers) {
           const int r = i / q, v = i % q;
-          if (4 * v < cols) cp_async16(smem_u32(wsm + r * p.CW + 4 * v), src + (size_t)r * p.E + 4 * v);
+          if (4 * v < cols)
+            cp_async16(smem_u32(wsm + r * p.CW + 4 * v), src + (size_t)r * p.E + 4 * v);
         }
       } else {
         for (int i = tid; i < len * p.CW; i += kWorkers) {
@@ -301,19 +304,32 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
           if (v < cols) cp_async4(smem_u32(wsm + r * p.CW + v), src + (size_t)r * p.E + v);
         }
       }
-      for (int i = tid; i < p.T * RR; i += kWorkers) {
-        const int t = i / RR, r = i % RR;
-        if (r < len) xs[i] = (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]);
+      // x as fp64, a row's tokens together: two a load below
+      for (int r = tid; r < len; r += kWorkers) {
+#pragma unroll 4
+        for (int t = 0; t < TT; ++t)
+          xs[r * TT + t] = t < p.T ? (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]) : 0.0;
       }
       cp_async_wait();
     }
     __syncthreads();
     if (worker && c < cols) {
-      for (int r = rg; r < len; r += nrg) {
-        const double w = (double)wsm[r * p.CW + c];
+      if (NBT == 1 && p.T == 1) {                // one chain of sums: read ahead of it
+#pragma unroll 8
+        for (int r = rg; r < len; r += nrg)
+          acc[0] = fma((double)wsm[r * p.CW + c], xs[r * TT], acc[0]);
+      } else {
+#pragma unroll 2
+        for (int r = rg; r < len; r += nrg) {
+          const double w = (double)wsm[r * p.CW + c];
+          const double2* x = reinterpret_cast<const double2*>(xs + r * TT);
 #pragma unroll
-        for (int t = 0; t < 8 * NBT; ++t)
-          if (t < p.T) acc[t] = fma(w, xs[t * RR + r], acc[t]);
+          for (int t = 0; t < TT / 2; ++t) {
+            const double2 v = x[t];
+            acc[2 * t] = fma(w, v.x, acc[2 * t]);
+            acc[2 * t + 1] = fma(w, v.y, acc[2 * t + 1]);
+          }
+        }
       }
     }
   }
@@ -321,7 +337,7 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
   double* red = reinterpret_cast<double*>(smem);                   // [T][kWorkers]
   if (worker) {
 #pragma unroll
-    for (int t = 0; t < 8 * NBT; ++t)
+    for (int t = 0; t < TT; ++t)
       if (t < p.T) red[t * kWorkers + tid] = acc[t];
   }
   __syncthreads();
@@ -330,6 +346,7 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
       const int t = i / p.CW, cc = i % p.CW;
       if (cc >= cols) continue;
       double s = 0.0;
+#pragma unroll 8
       for (int g = 0; g < nrg; ++g) s += red[t * kWorkers + g * p.CW + cc];
       p.rpart[((size_t)ks * p.T + t) * p.E + col0 + cc] = s;
     }
@@ -540,9 +557,9 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
     uint32_t* counter = p.sync + kSyncNext + 32 * down;
     int id = blockIdx.x;
     while (ok && id < ph.chunks) {
-      const ChunkInfo info = ph.info(id);
+      const ChunkInfo info = ph.info(sh, id);
       id = gridDim.x + (int)atomicAdd(counter, 1u);          // used when this chunk is issued
-      const int e = sh.expert[info.ac >> 16], col = (info.ac & 0xFFFF) * (down ? 4 : 2);
+      const int e = info.e, col = info.c * (down ? 4 : 2);
 #pragma unroll 1
       for (int i = 0; i < info.len; ++i) {
         if (!(ok = mbar_wait(&sh.empty[r.st], r.ph ^ 1, abort_flag))) break;
@@ -610,8 +627,7 @@ __device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem,
       if (!__all_sync(0xffffffffu, ok)) return false;
       waited = true;
     }
-    const int a = info.ac >> 16, c = info.ac & 0xFFFF;
-    const int row0 = sh.row0[a], n = sh.row0[a + 1] - row0;
+    const int c = info.c, row0 = info.row0, n = info.n;
     const int chunks = (DOWN && KIND == 0 ? 2 * n : n) * kChunks;
     // 16 bytes i of the rows: row, and place in its block
     auto src = [&](int i) {
@@ -630,7 +646,7 @@ __device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem,
       const int n0 = c * kTile + 8 * (DOWN ? lane : lane % 16);
       const FewMatrix& w = DOWN ? p.down : (lane / 16 ? p.up : p.gate);
       if (n0 < N)
-        scale = w.scale + ((size_t)sh.expert[a] * few_tiles(K, Cfg::G) +
+        scale = w.scale + ((size_t)info.e * few_tiles(K, Cfg::G) +
                            (size_t)info.kb0 * kScaleRows) * N + n0;
     }
 #pragma unroll 1
@@ -725,8 +741,8 @@ __device__ __forceinline__ void few_block(const uint8_t* stage, float (&acc)[2][
       for (int sub = 0; sub < 2; ++sub)
         w4[m][sub] = *reinterpret_cast<const uint4*>(codes + m * 8192 + sub * 2048);
 #pragma unroll
-    for (int j0 = 0; j0 < NBL; j0 += 3) {                // 3 token blocks at a time
-      constexpr int NJ = NBL < 3 ? NBL : 3;
+    for (int j0 = 0; j0 < NBL; j0 += (NBL > 3 ? 2 : NBL)) {  // a few token blocks at a time
+      constexpr int NJ = NBL > 3 ? 2 : NBL;
       uint32_t b[NJ][2][4];
       float u0[NJ], u1[NJ];
 #pragma unroll
@@ -776,17 +792,16 @@ __device__ __forceinline__ void few_block(const uint8_t* stage, float (&acc)[2][
 // its sums.  False when a wait gave up.
 template <int KIND, int NBT, int NBL, bool DOWN>
 __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const uint8_t* smem,
-                                          float* strip, Ring& r, const ChunkInfo& info, int n,
-                                          float* sums) {
+                                          float* strip, Ring& r, const ChunkInfo& info) {
   using Cfg = FewCfg<KIND, NBT>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int c = info.ac & 0xFFFF;
-  // strips past the matrix's width have nothing to do
-  const int c64 = (DOWN ? p.d : p.f) / 64 - c * (DOWN ? 4 : 2) - warp / 4;
-  const bool valid[2] = {c64 > 0, DOWN ? c64 > 2 : c64 > 0};
+  const int len = info.len, n = info.n;
+  // strips past the matrix's width have nothing to store
+  const int c64 = (DOWN ? p.d : p.f) / 64 - info.c * (DOWN ? 4 : 2) - warp / 4;
+  float* const sums = p.part + (size_t)info.sums * 256 + 16 * warp;
   float acc[2][NBL][4] = {};
 #pragma unroll 1
-  for (int i = 0; i < info.len; ++i) {
+  for (int i = 0; i < len; ++i) {
     if (i && !__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag)))
       return false;
     few_block<KIND, NBT, NBL>(smem + r.st * Cfg::kStageBytes, acc);
@@ -797,8 +812,8 @@ __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const
   const int g = lane / 4, q = lane % 4;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    if (!valid[m]) continue;
-    float* to = sums + m * 128 + 16 * warp;
+    if (c64 <= (DOWN ? 2 * m : 0)) continue;
+    float* to = sums + m * 128;
     if constexpr (KIND == 0 && !DOWN) {
 #pragma unroll
       for (int j = 0; j < NBL; ++j)
@@ -815,6 +830,17 @@ __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const
           __stcg(to + tok * 256 + g, acc[m][j][0] + acc[m][j][1]);
           __stcg(to + tok * 256 + g + 8, acc[m][j][2] + acc[m][j][3]);
         }
+      }
+    } else if constexpr (NBL == 1) {
+      // a token's three columns (its digits): token 0 in lanes q = 0 and 1,
+      // token 1 in q = 1 and 2
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float c0 = acc[m][0][2 * i], c1 = acc[m][0][2 * i + 1];
+        const float after = __shfl_down_sync(0xffffffffu, c0, 1);
+        const float before = __shfl_up_sync(0xffffffffu, c1, 1);
+        if (q == 0) __stcg(to + g + 8 * i, after + (c1 + c0));
+        if (q == 2 && n > 1) __stcg(to + 256 + g + 8 * i, c1 + (c0 + before));
       }
     } else {
       // a token's three columns: its digits; 8 tokens at a time through the
@@ -847,10 +873,10 @@ __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const
 // All chunks of a phase that this CTA takes.
 template <int KIND, int NBT, bool DOWN>
 __device__ __forceinline__ bool few_phase(const FewArgs& p, FewShared& sh, const uint8_t* smem,
-                                          float* strip, Ring& r, const Phase& ph) {
+                                          float* strip, Ring& r) {
   using Cfg = FewCfg<KIND, NBT>;
   constexpr int NB = DOWN ? Cfg::kColsD : Cfg::kColsG;
-  constexpr int kPerToken = KIND ? 3 : (DOWN ? 2 : 1);
+  constexpr int kPerToken = KIND ? 3 : (DOWN ? 2 : 1), kMid = KIND ? 3 : 4;
 #pragma unroll 1
   while (true) {
     if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag))) return false;
@@ -861,38 +887,29 @@ __device__ __forceinline__ bool few_phase(const FewArgs& p, FewShared& sh, const
       r.next(Cfg::kStages);
       return true;
     }
-    const int a = info.ac >> 16, n = sh.row0[a + 1] - sh.row0[a];
-    float* sums = p.part + ph.sums_at(sh, a, info.ac & 0xFFFF, n) +
-                  (size_t)(info.kb0 / ph.len) * n * 256;
-    const int nb = (n * kPerToken + 7) / 8;
+    const int nb = (info.n * kPerToken + 7) / 8;
     bool ok;
     // as wide as needed: 1, 2, 4, 8 blocks (bf16), 1, 2, 3, 6, 12 (digits)
-    if (nb == 1)
-      ok = few_chunk<KIND, NBT, 1, DOWN>(p, sh, smem, strip, r, info, n, sums);
-    else if (nb == 2)
-      ok = few_chunk<KIND, NBT, (NB < 2 ? 1 : 2), DOWN>(p, sh, smem, strip, r, info, n, sums);
-    else if (nb <= (KIND ? 3 : 4))
-      ok = few_chunk<KIND, NBT, (KIND ? 3 : (NB < 4 ? NB : 4)), DOWN>(p, sh, smem, strip, r, info,
-                                                                     n, sums);
-    else if (nb <= (KIND ? 6 : 8))
-      ok = few_chunk<KIND, NBT, (KIND ? (NB < 6 ? NB : 6) : NB), DOWN>(p, sh, smem, strip, r, info,
-                                                                     n, sums);
-    else
-      ok = few_chunk<KIND, NBT, NB, DOWN>(p, sh, smem, strip, r, info, n, sums);
+    if (nb == 1) {
+      ok = few_chunk<KIND, NBT, 1, DOWN>(p, sh, smem, strip, r, info);
+    } else if (NB == 2 || (NB > 2 && nb == 2)) {
+      ok = few_chunk<KIND, NBT, (NB < 2 ? 1 : 2), DOWN>(p, sh, smem, strip, r, info);
+    } else if (NB == kMid || (NB > kMid && nb <= kMid)) {
+      ok = few_chunk<KIND, NBT, (NB < kMid ? 1 : kMid), DOWN>(p, sh, smem, strip, r, info);
+    } else if (NB == 2 * kMid || (NB > 2 * kMid && nb <= 2 * kMid)) {
+      ok = few_chunk<KIND, NBT, (NB < 2 * kMid ? 1 : 2 * kMid), DOWN>(p, sh, smem, strip, r, info);
+    } else {
+      ok = few_chunk<KIND, NBT, (NB > 2 * kMid ? NB : 1), DOWN>(p, sh, smem, strip, r, info);
+    }
     if (!ok) return false;
   }
 }
 
-// The sums of row r's unit in column tile c, from column `col` on: where they
-// start, and how far apart the chunks' are.
-struct Sums {
-  const float* at;
-  size_t step;
-};
-__device__ __forceinline__ Sums few_sums(const FewArgs& p, const FewShared& sh, const Phase& ph,
-                                         int r, int c, int col) {
-  const int a = sh.row_a[r], n = sh.row0[a + 1] - sh.row0[a];
-  return {p.part + ph.sums_at(sh, a, c, n) + (r - sh.row0[a]) * 256 + col, (size_t)n * 256};
+// The sums of row r's unit in column tile c: where they start, and how far apart
+// the chunks' are, in tokens of 256 floats.
+__device__ __forceinline__ int2 few_sums(const FewShared& sh, const Phase& ph, int r, int c) {
+  const int a = sh.row_a[r], row0 = sh.row0[a], n = sh.row0[a + 1] - row0;
+  return make_int2(ph.tile_at(row0, n, c) + r - row0, n);
 }
 
 // h of one row in one tile of 128 columns, by one warp: lane -> columns 2 c,
@@ -902,12 +919,13 @@ __device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, in
   const int lane = threadIdx.x % 32;
   const int at = (lane / 4) * 16 + 2 * (lane % 4);
   const bool valid = c * 128 + at < p.f;
-  const Sums s = few_sums(p, sh, ph, row, c, at);
+  const int2 s = few_sums(sh, ph, row, c);
+  const float* src = p.part + (size_t)s.x * 256 + at;
+  const size_t step = (size_t)s.y * 256;
   float g[4] = {}, u[4] = {};
   if (valid) {
 #pragma unroll 8
-    for (int i = 0; i < ph.q; ++i) {
-      const float* src = s.at + i * s.step;
+    for (int i = 0; i < ph.q; ++i, src += step) {
       const float2 g0 = __ldcg(reinterpret_cast<const float2*>(src));
       const float2 g1 = __ldcg(reinterpret_cast<const float2*>(src + 8));
       const float2 u0 = __ldcg(reinterpret_cast<const float2*>(src + 128));
@@ -947,23 +965,44 @@ __device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, in
 // weighted sums are added last.
 __device__ void few_combine(const FewArgs& p, const FewShared& sh, const Phase& ph, int t,
                             int col32) {
+  constexpr int kBatch = 8;                  // loads in flight
   const int lane = threadIdx.x % 32;
-  const int col = 32 * col32 + 4 * (lane % 8), c = col / 256;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool any = false;
-  for (int j = 0; j < p.k; ++j) any = any || sh.pair_row[t * p.k + j] >= 0;
+  const int col = 32 * col32 + 4 * (lane % 8);
+  const int c = col / 256;
+  // lane j < k: row j of the token
+  const int row = lane < p.k ? sh.pair_row[t * p.k + lane] : -1;
+  const float weight = lane < p.k ? sh.pair_w[t * p.k + lane] : 0.f;
+  const int2 at = row >= 0 ? few_sums(sh, ph, row, c) : make_int2(0, 0);
+  const bool any = __any_sync(0xffffffffu, row >= 0);
+  const float* base = p.part + col % 256;
   const int terms = p.k * ph.q;
-#pragma unroll 8
-  for (int i = lane / 8; i < terms; i += 4) {
-    const int j = i / ph.q, row = sh.pair_row[t * p.k + j];
-    if (row < 0) continue;
-    const Sums s = few_sums(p, sh, ph, row, c, col % 256);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(s.at + (i - j * ph.q) * s.step));
-    const float w = sh.pair_w[t * p.k + j];
-    y.x = fmaf(w, v.x, y.x);
-    y.y = fmaf(w, v.y, y.y);
-    y.z = fmaf(w, v.z, y.z);
-    y.w = fmaf(w, v.w, y.w);
+  const float inv_q = 1.0f / (float)ph.q;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = lane / 8; i0 - lane / 8 < terms; i0 += 4 * kBatch) {
+    float4 v[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + 4 * u;
+      const int j = (int)(((float)i + 0.5f) * inv_q);        // i / q: exact, i < 2^16
+      const int r = __shfl_sync(0xffffffffu, row, j % 32);
+      const int x = __shfl_sync(0xffffffffu, at.x, j % 32);
+      const int n = __shfl_sync(0xffffffffu, at.y, j % 32);
+      w[u] = __shfl_sync(0xffffffffu, weight, j % 32);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < terms && r >= 0)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(
+            base + (size_t)(x + (i - j * ph.q) * n) * 256));
+      else
+        w[u] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      y.x = fmaf(w[u], v[u].x, y.x);
+      y.y = fmaf(w[u], v[u].y, y.y);
+      y.z = fmaf(w[u], v[u].z, y.z);
+      y.w = fmaf(w[u], v[u].w, y.w);
+    }
   }
 #pragma unroll
   for (int o = 8; o < 32; o <<= 1) {
@@ -1006,7 +1045,7 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
                  warp * 16 * kStripPitch;
   Ring r;
   const Phase up(sh, p.T, p.k, few_tiles(p.f, 128), few_tiles(p.d, Cfg::KB));
-  bool ok = few_phase<KIND, NBT, false>(p, sh, smem, strip, r, up);
+  bool ok = few_phase<KIND, NBT, false>(p, sh, smem, strip, r);
   if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
   few_arrive(sh, p.sync + kSyncG);
 
@@ -1020,7 +1059,7 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
   few_arrive(sh, p.sync + kSyncH);
 
   const Phase down(sh, p.T, p.k, few_tiles(p.d, 256), few_tiles(p.f, Cfg::KB));
-  ok = ok && few_phase<KIND, NBT, true>(p, sh, smem, strip, r, down);
+  ok = ok && few_phase<KIND, NBT, true>(p, sh, smem, strip, r);
   if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
   few_arrive(sh, p.sync + kSyncY);
 
