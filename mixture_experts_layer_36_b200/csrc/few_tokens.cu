@@ -38,19 +38,20 @@
 
 namespace moe {
 
-constexpr int kFewWarps = 8;                       // consumers: two 16-column strips a warp
-constexpr int kWorkers = 32 * kFewWarps;
-constexpr int kFewThreads = kWorkers + 64;         // and two producer warps
+// A team: 8 consumer warps with two 16-column strips of a tile each, a thread
+// that issues the weights' copies and a warp that loads token rows, with a ring
+// of stages and a row of chunks of its own.  bf16 blocks leave one team idle
+// half the time; on codes two teams hide one another's latencies (8 warps: 480
+// clocks a block at one token block, 680 at three; 2 x 8: 330 and 630).
+constexpr int kTeamWarps = 8;
 constexpr int kFewMaxPairs = MOE_FEW_MAX_TOKENS * 8;
 constexpr int kFewRouterRows = 384;                // router rows staged at once
 constexpr int kFewMaxSplits = 32;
 constexpr int kFewMaxStages = 10;
-constexpr int kStripPitch = 26;
 constexpr int kDigitBytes = 3 * 144;               // 128 values of a token as int8 digits
 
-// A phase is cut into about kChunksPerCta chunks a CTA, of kMinChunk blocks or
-// more; sums of at most T*k*tiles + kPartRows(T) tile rows (1 KB each) are kept.
-constexpr int kChunksPerCta = 16, kMinChunk = 2;
+// The chunks of a phase keep sums of at most T*k*tiles + few_part_rows(T) tile
+// rows (1 KB each).
 inline __host__ __device__ int few_part_rows(int T) { return 2560 * (T < 4 ? T : 4); }
 
 // grid-wide counters, zeroed by the call, each on its own line: arrivals of the
@@ -64,6 +65,9 @@ constexpr int kSyncRouter = 0, kSyncRouted = 32, kSyncG = 64, kSyncH = 96, kSync
 // as three rows of int8 digits (codes; few_digits below).
 template <int KIND, int NBT>
 struct FewCfg {
+  static constexpr int kTeams = KIND == 0 ? 1 : 2;
+  static constexpr int kWorkers = 32 * kTeamWarps * kTeams;      // consumer threads
+  static constexpr int kThreads = kWorkers + 64 * kTeams;
   static constexpr int KB = KIND == 0 ? 64 : 128;         // rows of a block
   static constexpr int G = 256 >> KIND;                   // rows of a group (codes)
   static constexpr int kWBytes = KIND == 0 ? 32768 : 16384;
@@ -71,26 +75,38 @@ struct FewCfg {
   // a token row: 128 bytes of values, 16 of padding, which keep ldmatrix free
   // of bank conflicts (and hold the scale of the digits)
   static constexpr int kPitch = 144;
-  static constexpr int kRows = (KIND == 0 ? 16 : 24) * NBT;
-  static constexpr int kColsG = KIND == 0 ? NBT : 3 * NBT;      // most 8-column blocks
-  static constexpr int kColsD = KIND == 0 ? 2 * NBT : 3 * NBT;
+  // tokens of a unit: with codes, an expert with more has several units, whose
+  // chunks run side by side and find the weights in L2 (a block's time grows
+  // with its tokens there, and two teams leave 96 registers a thread)
+  static constexpr int kUnitTokens = KIND != 0 ? 8 : 8 * NBT;
+  static constexpr int kRows = (KIND == 0 ? 2 : 3) * kUnitTokens;
+  static constexpr int kColsG = (KIND == 0 ? 1 : 3) * kUnitTokens / 8;   // most 8-column blocks
+  static constexpr int kColsD = (KIND == 0 ? 2 : 3) * kUnitTokens / 8;
   static constexpr int kStageBytes =
       (kWBytes + kScaleBytes + kRows * kPitch + 1023) / 1024 * 1024;
-  // codes: a warp's sums of a token's digits meet here
-  static constexpr int kStripBytes = KIND == 0 ? 0 : kFewWarps * 16 * kStripPitch * 4;
-  static constexpr int kFit = (224256 - kStripBytes) / kStageBytes;
-  static constexpr int kStages = kFit > kFewMaxStages ? kFewMaxStages : kFit;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kStripBytes + 1024;
+  static constexpr int kFit = 224256 / kStageBytes / kTeams;
+  static constexpr int kStages = kFit > kFewMaxStages / 2 * (3 - kTeams)
+                                     ? kFewMaxStages / 2 * (3 - kTeams) : kFit;   // of a team
+  static constexpr int kSmemBytes = kTeams * kStages * kStageBytes + 1024;
   // the router's staging uses the same memory: x (fp64), then W rows
   static constexpr int kXsBytes = 8 * NBT * kFewRouterRows * 8;
-  static_assert(kXsBytes + kFewRouterRows * 32 * 4 <= kStages * kStageBytes, "router staging");
-  static_assert(kWorkers * 8 * NBT * 8 <= kStages * kStageBytes, "router reduction");
+  static_assert(kXsBytes + kFewRouterRows * 32 * 4 < kSmemBytes - 1024, "router staging");
+  static_assert(kWorkers * 8 * NBT * 8 < kSmemBytes - 1024, "router reduction");
 };
 
 // The chunk whose first block a stage holds (len 0: the phase is over).
 struct alignas(16) ChunkInfo {
   int len, kb0, a, c;                 // blocks, the first one; active expert, column tile
   int n, row0, e, sums;               // its rows and expert; where its sums go (1 KB each)
+};
+
+// How a phase is cut: column tiles, blocks of a unit, blocks of a chunk, chunks
+// of a unit, of the phase.
+struct Phase {
+  int nct, nkb, len, q, chunks;
+  // Where the sums of chunk 0 of a unit lie, in tokens of 256 floats (1 KB); the
+  // next chunk's are n further.
+  __device__ int tile_at(int row0, int n, int c) const { return (row0 * nct + c * n) * q; }
 };
 
 struct FewShared {
@@ -100,9 +116,11 @@ struct FewShared {
   ChunkInfo info[kFewMaxStages];
   int abort_flag, never, ok;
   uint32_t mask[256];                 // tokens that chose expert e
-  uint16_t row0[257];                 // first kept row of active expert a
+  uint16_t row0[257];                 // first kept row of active expert a (with codes: of
+                                      // at most 8 rows of one; so for all a below)
   uint8_t expert[256];                // active expert a -> e
-  uint8_t active[256];                // e -> a
+  uint8_t active[256];                // e -> its first a
+  uint8_t part0[256], parts[256];     // a -> the first a of its expert, and their number
   uint8_t row_tok[kFewMaxPairs];      // kept row -> token
   uint8_t row_a[kFewMaxPairs];        // kept row -> active expert
   int16_t pair_row[kFewMaxPairs];     // pair -> kept row, -1 dropped
@@ -110,6 +128,7 @@ struct FewShared {
   float logit[256];
   uint32_t warp_sum[8];
   int A;                              // active experts
+  Phase phase[2];                     // G, D
 };
 
 // ---------------------------------------------------------------- small pieces
@@ -127,7 +146,7 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -147,26 +166,30 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ void red_release(uint32_t* p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
 // order this thread's and (through barriers) other threads' generic accesses
 // with asynchronous copies of the same memory
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
+template <int N>
 __device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 // c = products + (first ? init : c)
 __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1, bool first,
                                        int init) {
   if (first)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(init));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
@@ -236,43 +259,63 @@ __device__ __forceinline__ bool wait_count(const uint32_t* c, uint32_t target,
   }
 }
 
-// The chunks of a phase.
-struct Phase {
-  int nct, nkb, len, q, chunks;       // column tiles, blocks of a unit, blocks of a chunk,
-                                      // chunks of a unit, of the phase
-  __device__ Phase(const FewShared& sh, int T, int k, int nct_, int nkb_) : nct(nct_), nkb(nkb_) {
-    const long long total = (long long)sh.A * nct * nkb;
-    const long long want = (total + gridDim.x * kChunksPerCta - 1) / (gridDim.x * kChunksPerCta);
-    len = (int)min((long long)nkb, max(want, (long long)kMinChunk));
-    q = (nkb + len - 1) / len;
-    const int rows = sh.row0[sh.A] * nct;
-    q = min(q, (T * k * nct + few_part_rows(T)) / rows);      // 1 or more: rows <= T k nct
-    len = (nkb + q - 1) / q;
-    q = (nkb + len - 1) / len;
-    chunks = sh.A * nct * q;
-  }
-  __device__ ChunkInfo info(const FewShared& sh, int id) const {
-    const int u = id / q, a = u / nct, qi = id - u * q;
-    ChunkInfo i;
-    i.a = a;
-    i.c = u - a * nct;
-    i.kb0 = qi * len;
-    i.len = min(len, nkb - i.kb0);
-    i.row0 = sh.row0[a];
-    i.n = sh.row0[a + 1] - i.row0;
-    i.e = sh.expert[a];
-    i.sums = tile_at(i.row0, i.n, i.c) + qi * i.n;
-    return i;
-  }
-  // Where the sums of chunk 0 of a unit lie, in tokens of 256 floats (1 KB); the
-  // next chunk's are n further.
-  __device__ int tile_at(int row0, int n, int c) const { return (row0 * nct + c * n) * q; }
-};
 __device__ __forceinline__ int few_tiles(int width, int tile) { return (width + tile - 1) / tile; }
+
+__device__ __forceinline__ ChunkInfo chunk_info(const FewShared& sh, const Phase& ph, int id) {
+  // an expert's units take turns, so that they read the same weights together
+  const int f = sh.part0[id / (ph.q * ph.nct)], m = sh.parts[f];
+  const int in = id - f * ph.nct * ph.q, chunk = in / m, a = f + in - chunk * m;
+  ChunkInfo i;
+  i.a = a;
+  i.c = chunk / ph.q;
+  const int qi = chunk - i.c * ph.q;
+  i.kb0 = qi * ph.len;
+  i.len = min(ph.len, ph.nkb - i.kb0);
+  i.row0 = sh.row0[a];
+  i.n = sh.row0[a + 1] - i.row0;
+  i.e = sh.expert[a];
+  i.sums = ph.tile_at(i.row0, i.n, i.c) + qi * i.n;
+  return i;
+}
+
+// The cut of a phase, by one warp: each lane weighs two chunk lengths by the
+// time of the team with the most chunks, in sixteenths of a block's time, a chunk
+// costing kChunkCost on top of its blocks.
+constexpr int kChunkCostBf16 = 32, kChunkCostCodes = 30;
+__device__ void few_cut(const FewArgs& p, FewShared& sh, int which, int nct, int nkb, bool codes) {
+  const int lane = threadIdx.x % 32;
+  const unsigned teams = gridDim.x * (codes ? 2 : 1);
+  const int units = sh.A * nct, rows = sh.row0[sh.A] * nct;
+  const int q_max = (p.T * p.k * nct + few_part_rows(p.T)) / rows;     // 1 or more
+  unsigned best = 0xFFFFFFFFu;
+  int best_len = nkb;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // lengths of 1 to 32 blocks, and units cut in 1 to 32
+    const int len = min(nkb, i ? (nkb + lane) / (lane + 1) : lane + 1);
+    const int q = (nkb + len - 1) / len;
+    const unsigned rounds = ((unsigned)units * q + teams - 1) / teams;
+    const unsigned long long cost =
+        (unsigned long long)rounds * (16u * len + (codes ? kChunkCostCodes : kChunkCostBf16)) +
+        (codes ? 8u * len : 0u);
+    const unsigned c = q > q_max || cost > 0x7FFFFFFFull ? 0xFFFFFFFEu : (unsigned)cost;
+    if (c < best) {
+      best = c;
+      best_len = len;
+    }
+  }
+  const unsigned least = __reduce_min_sync(0xffffffffu, best);
+  const unsigned len = __reduce_max_sync(0xffffffffu, best == least ? (unsigned)best_len : 0u);
+  if (lane == 0) {
+    // no candidate within bounds (units longer than 32 q_max blocks): whole units
+    const int l = least >= 0xFFFFFFFEu ? nkb : (int)len, q = (nkb + l - 1) / l;
+    sh.phase[which] = Phase{nct, nkb, l, q, units * q};
+  }
+}
 
 // ---------------------------------------------------------------- R: router
 // Partial sums of this CTA's rows and columns for all tokens, in fp64.
-template <int NBT>
+template <int NBT, int kWorkers>
 __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
   constexpr int RR = kFewRouterRows, TT = 8 * NBT;
   const int tid = threadIdx.x;
@@ -382,9 +425,8 @@ __device__ __forceinline__ void put_digits(uint8_t* out, const float (&x)[4]) {
 // The digits of the tokens.
 __device__ void few_digits(const FewArgs& p) {
   const int lane = threadIdx.x % 32, nkb = (p.d + 127) / 128;
-  if (threadIdx.x >= kWorkers) return;
   for (int i = threadIdx.x / 32 * gridDim.x + blockIdx.x; i < p.T * nkb;
-       i += kFewWarps * gridDim.x) {
+       i += blockDim.x / 32 * gridDim.x) {
     const int t = i / nkb, kb = i - t * nkb;
     const int at = kb * 128 + (lane / 4) * 16 + 2 * (lane % 4);
     uint32_t lo = 0, hi = 0;
@@ -451,14 +493,14 @@ __device__ void few_route_token(const FewArgs& p, FewShared& sh, int t) {
       p.topk_idx[t * p.k + tid] = my_e;
       p.topk_w[t * p.k + tid] = mine / sum;
     }
-    __threadfence();
     __syncwarp();
-    if (tid == 0) atomicAdd(p.sync + kSyncRouted, 1u);
+    if (tid == 0) red_release(p.sync + kSyncRouted);
   }
   __syncthreads();
 }
 
 // Which experts run and on which tokens: every CTA builds the same tables.
+template <int kUnitTokens>
 __device__ void few_tables(const FewArgs& p, FewShared& sh) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int pairs = p.T * p.k;
@@ -475,7 +517,7 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
   uint32_t n = 0, v = 0, incl = 0;
   if (tid < 256) {
     n = min(__popc(sh.mask[tid]), p.C);
-    v = n | (n ? 1u << 16 : 0u);
+    v = n | (n + kUnitTokens - 1) / kUnitTokens << 16;
     incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -491,9 +533,14 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
     const uint32_t excl = before + incl - v;
     if (n) {
       const int a = (int)(excl >> 16);
-      sh.expert[a] = (uint8_t)tid;
       sh.active[tid] = (uint8_t)a;
-      sh.row0[a] = (uint16_t)(excl & 0xFFFF);
+      const int parts = ((int)n + kUnitTokens - 1) / kUnitTokens;
+      for (int i = 0; i < parts; ++i) {
+        sh.part0[a + i] = (uint8_t)a;
+        sh.parts[a + i] = (uint8_t)parts;
+        sh.expert[a + i] = (uint8_t)tid;
+        sh.row0[a + i] = (uint16_t)((excl & 0xFFFF) + i * kUnitTokens);
+      }
     }
     if (tid == 255) {
       const uint32_t all = before + incl;
@@ -510,7 +557,7 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
     sh.pair_row[tid] = (int16_t)row;
     if (kept) {
       sh.row_tok[row] = (uint8_t)t;
-      sh.row_a[row] = sh.active[e];
+      sh.row_a[row] = (uint8_t)(sh.active[e] + slot / kUnitTokens);
     }
     if (blockIdx.x == 0) p.slot[tid] = kept ? slot : -1;
   }
@@ -518,13 +565,16 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh) {
 }
 
 // ---------------------------------------------------------------- producers
+// A team's ring: stages base .. base + stages - 1.
+template <int S>
 struct Ring {
-  int st = 0, n = 0;
+  int base, st, n = 0;
   uint32_t ph = 0;
-  __device__ void next(int stages) {
+  __device__ explicit Ring(int team) : base(team * S), st(team * S) {}
+  __device__ void next() {
     ++n;
-    if (++st == stages) {
-      st = 0;
+    if (++st == base + S) {
+      st = base;
       ph ^= 1;
     }
   }
@@ -541,24 +591,23 @@ __device__ __forceinline__ bool elect_one() {
 // One thread takes chunks and issues the weights' copies, one TMA box a matrix
 // and block.  It runs into phase D on its own: nothing it reads depends on G.
 template <int KIND, int NBT>
-__device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
+__device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem, int team,
                             const CUtensorMap* tmG, const CUtensorMap* tmU,
                             const CUtensorMap* tmD) {
   using Cfg = FewCfg<KIND, NBT>;
   constexpr int S = Cfg::kStages;
   volatile int* abort_flag = &sh.abort_flag;
   constexpr int kAt = KIND == 0 ? 64 : 4;      // box rows: 64 of bf16, 4 KB chunks of codes
-  Ring r;
+  Ring<S> r(team);
   bool ok = true;
 #pragma unroll 1
   for (int down = 0; ok && down < 2; ++down) {
-    const Phase ph(sh, p.T, p.k, few_tiles(down ? p.d : p.f, down ? 256 : 128),
-                   few_tiles(down ? p.f : p.d, Cfg::KB));
+    const Phase ph = sh.phase[down];
     uint32_t* counter = p.sync + kSyncNext + 32 * down;
-    int id = blockIdx.x;
+    int id = blockIdx.x + team * gridDim.x;
     while (ok && id < ph.chunks) {
-      const ChunkInfo info = ph.info(sh, id);
-      id = gridDim.x + (int)atomicAdd(counter, 1u);          // used when this chunk is issued
+      const ChunkInfo info = chunk_info(sh, ph, id);
+      id = Cfg::kTeams * gridDim.x + (int)atomicAdd(counter, 1u);    // used when this chunk is issued
       const int e = info.e, col = info.c * (down ? 4 : 2);
 #pragma unroll 1
       for (int i = 0; i < info.len; ++i) {
@@ -575,7 +624,7 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
           tma_load_4d(stage, tmG, bar, 0, at, col, e);
           tma_load_4d(stage + Cfg::kWBytes / 2, tmU, bar, 0, at, col, e);
         }
-        r.next(S);
+        r.next();
       }
     }
     // the phase is over
@@ -583,7 +632,7 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
       sh.info[r.st].len = 0;
       mbar_arrive(&sh.ready[r.st]);
       mbar_arrive(&sh.full[r.st]);
-      r.next(S);
+      r.next();
     }
   }
   if (!ok) {
@@ -593,7 +642,7 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
   // every copy has landed before the CTA may exit
   for (int back = 1; back <= S && back <= r.n; ++back) {
     const int it = r.n - back;
-    if (!mbar_wait(&sh.full[it % S], (it / S) & 1, &sh.never)) break;
+    if (!mbar_wait(&sh.full[r.base + it % S], (it / S) & 1, &sh.never)) break;
   }
 }
 
@@ -601,7 +650,8 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem,
 // lanes: their pieces are small, and a bulk copy each took 150 clocks to issue,
 // which bound the stream at 60 % of the HBM rate.
 template <int KIND, int NBT, bool DOWN>
-__device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem, Ring& r) {
+__device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem,
+                                 Ring<FewCfg<KIND, NBT>::kStages>& r) {
   using Cfg = FewCfg<KIND, NBT>;
   constexpr int kTile = DOWN ? 256 : 128;
   constexpr int kScaleRows = KIND ? Cfg::KB / Cfg::G : 0;
@@ -619,7 +669,7 @@ __device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem,
     const ChunkInfo info = sh.info[r.st];
     if (info.len == 0) {
       mbar_arrive(&sh.full[r.st]);
-      r.next(Cfg::kStages);
+      r.next();
       return true;
     }
     if (!waited) {                                          // h of all tokens is there
@@ -676,14 +726,14 @@ __device__ bool few_tokens_phase(const FewArgs& p, FewShared& sh, uint8_t* smem,
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                        smem_u32(&sh.full[r.st]))
                    : "memory");
-      r.next(Cfg::kStages);
+      r.next();
     }
   }
 }
 
 template <int KIND, int NBT>
-__device__ void few_tokens(const FewArgs& p, FewShared& sh, uint8_t* smem) {
-  Ring r;
+__device__ void few_tokens(const FewArgs& p, FewShared& sh, uint8_t* smem, int team) {
+  Ring<FewCfg<KIND, NBT>::kStages> r(team);
   bool ok = few_tokens_phase<KIND, NBT, false>(p, sh, smem, r);
   ok = ok && few_tokens_phase<KIND, NBT, true>(p, sh, smem, r);
   if (!ok && threadIdx.x % 32 == 0) {
@@ -699,91 +749,130 @@ __device__ void few_tokens(const FewArgs& p, FewShared& sh, uint8_t* smem) {
 // up).  NBL: token blocks.  Rows past the matrix's end hold zero weights (bf16)
 // or zero digits, columns past it give sums that nobody stores: no block needs
 // a branch (conditions on either cost a thousand bytes of register spills).
-template <int KIND, int NBT, int NBL>
-__device__ __forceinline__ void few_block(const uint8_t* stage, float (&acc)[2][NBL][4]) {
-  using Cfg = FewCfg<KIND, NBT>;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rows = smem_u32(stage + Cfg::kWBytes + Cfg::kScaleBytes) +
-                        (lane % 8) * Cfg::kPitch + (lane / 8) * 16;
-  if constexpr (KIND == 0) {
-    const int chunk = 2 * (warp % 4) + ((lane / 8) & 1);
-    // row k of a swizzled tile: 128 k, its 16-byte chunk c at c ^ (k % 8)
-    const uint32_t at = smem_u32(stage) + (warp / 4) * 8192 + ((lane / 16) * 8 + lane % 8) * 128 +
-                        ((chunk ^ (lane % 8)) << 4);
+template <int NBT, int NBL>
+__device__ __forceinline__ void few_block_bf16(const uint8_t* stage, float (&acc)[2][NBL][4]) {
+  using Cfg = FewCfg<0, NBT>;
+  const int warp = threadIdx.x / 32 % kTeamWarps, lane = threadIdx.x % 32;
+  const uint32_t rows =
+      smem_u32(stage + Cfg::kWBytes) + (lane % 8) * Cfg::kPitch + (lane / 8) * 16;
+  const int chunk = 2 * (warp % 4) + ((lane / 8) & 1);
+  // row k of a swizzled tile: 128 k, its 16-byte chunk c at c ^ (k % 8)
+  const uint32_t at = smem_u32(stage) + (warp / 4) * 8192 + ((lane / 16) * 8 + lane % 8) * 128 +
+                      ((chunk ^ (lane % 8)) << 4);
 #pragma unroll
-    for (int s2 = 0; s2 < 2; ++s2) {
-      uint32_t b[NBL][4];
+  for (int s2 = 0; s2 < 2; ++s2) {
+    uint32_t b[NBL][4];
 #pragma unroll
-      for (int j = 0; j < NBL; ++j) ldsm4(b[j], rows + j * 8 * Cfg::kPitch + s2 * 64);
+    for (int j = 0; j < NBL; ++j) ldsm4(b[j], rows + j * 8 * Cfg::kPitch + s2 * 64);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t a[4];
-          ldsm4_trans(a, at + m * 16384 + (2 * s2 + s) * 2048);
-#pragma unroll
-          for (int j = 0; j < NBL; ++j) mma_bf16(acc[m][j], a, b[j][2 * s], b[j][2 * s + 1]);
-        }
-    }
-  } else {
-    constexpr float kMagic = 12582912.f;                // 1.5 2^23: sums start as its bits
-    constexpr int kMagicBits = 0x4B400000;
-    constexpr int kGroups = Cfg::KB / Cfg::G, kPer = 4 / kGroups;    // groups; k32 steps of one
-    const uint8_t* codes = stage + (warp / 4) * 4096 + (warp % 4) * 512 + lane * 16;
-    const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(stage + Cfg::kWBytes) +
-                              16 * warp + lane / 4;
-    const uint8_t* unit = stage + Cfg::kWBytes + Cfg::kScaleBytes + 128 + (lane % 4) * 2 * 144;
-    // both strips' words first: their loads overlap
-    uint4 w4[2][2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-        w4[m][sub] = *reinterpret_cast<const uint4*>(codes + m * 8192 + sub * 2048);
-#pragma unroll
-    for (int j0 = 0; j0 < NBL; j0 += (NBL > 3 ? 2 : NBL)) {  // a few token blocks at a time
-      constexpr int NJ = NBL > 3 ? 2 : NBL;
-      uint32_t b[NJ][2][4];
-      float u0[NJ], u1[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        ldsm4(b[j][0], rows + (j0 + j) * 8 * Cfg::kPitch);
-        ldsm4(b[j][1], rows + (j0 + j) * 8 * Cfg::kPitch + 64);
-        u0[j] = *reinterpret_cast<const float*>(unit + (j0 + j) * 8 * 144);
-        u1[j] = *reinterpret_cast<const float*>(unit + (j0 + j) * 8 * 144 + 144);
-      }
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        int t[NJ][4];
+        uint32_t a[4];
+        ldsm4_trans(a, at + m * 16384 + (2 * s2 + s) * 2048);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const uint4& w = w4[m][h / 2];
-          const uint32_t lo = h % 2 ? w.z : w.x, hi = h % 2 ? w.w : w.y;
-          // even nibbles: column g; odd ones: column g + 8; 16 (u - 8) as int8
-          const uint32_t a0 = and_xor(lo << 4, 0xF0F0F0F0u, 0x80808080u);
-          const uint32_t a1 = and_xor(lo, 0xF0F0F0F0u, 0x80808080u);
-          const uint32_t a2 = and_xor(hi << 4, 0xF0F0F0F0u, 0x80808080u);
-          const uint32_t a3 = and_xor(hi, 0xF0F0F0F0u, 0x80808080u);
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            mma_s8(t[j], a0, a1, a2, a3, b[j][h / 2][h % 2 * 2], b[j][h / 2][h % 2 * 2 + 1],
-                   h % kPer == 0, kMagicBits);
-          // the group's integer sums, scaled, into the fp32 sums
-          if (h % kPer == kPer - 1) {
-            const int g = kGroups == 1 ? 0 : h / kPer;
-            const float s0 = __bfloat162float(sc[g * 256 + m * 128]);
-            const float s1 = __bfloat162float(sc[g * 256 + m * 128 + 8]);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              float(&c)[4] = acc[m][j0 + j];
-              c[0] = fmaf((__int_as_float(t[j][0]) - kMagic) * u0[j], s0, c[0]);
-              c[1] = fmaf((__int_as_float(t[j][1]) - kMagic) * u1[j], s0, c[1]);
-              c[2] = fmaf((__int_as_float(t[j][2]) - kMagic) * u0[j], s1, c[2]);
-              c[3] = fmaf((__int_as_float(t[j][3]) - kMagic) * u1[j], s1, c[3]);
-            }
-          }
-        }
+        for (int j = 0; j < NBL; ++j) mma_bf16(acc[m][j], a, b[j][2 * s], b[j][2 * s + 1]);
       }
+  }
+}
+
+// Two fp32 values at a time (one instruction each on sm_100a).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(int lo, int hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The same on codes; acc[m][j][i]: row half i (columns g, g + 8 of the strip),
+// two token columns.  A block's sums are integers, which scale and join the fp32
+// sums group by group: that arithmetic, not the products, was half of a block's
+// time before it was done two values an instruction (8 warps, one token block:
+// 430 clocks a block with groups of 128, 590 with 64, of the 720 that HBM
+// leaves).
+template <int KIND, int NBT, int NBL>
+__device__ __forceinline__ void few_block_codes(const uint8_t* stage, uint64_t (&acc)[2][NBL][2]) {
+  using Cfg = FewCfg<KIND, NBT>;
+  constexpr int kMagicBits = 0x4B400000;                // 1.5 2^23: sums start as its bits
+  constexpr int kGroups = Cfg::KB / Cfg::G, kPer = 4 / kGroups;      // groups; k32 steps of one
+  constexpr int kRowsAt = Cfg::kWBytes + Cfg::kScaleBytes;
+  const int warp = threadIdx.x / 32 % kTeamWarps, lane = threadIdx.x % 32;
+  const uint8_t* codes = stage + (warp / 4) * 4096 + (warp % 4) * 512 + lane * 16;
+  const uint32_t rows = smem_u32(stage + kRowsAt) + (lane % 8) * Cfg::kPitch + (lane / 8) * 16;
+  const uint8_t* units = stage + kRowsAt + 128 + (lane % 4) * 2 * Cfg::kPitch;
+  const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(stage + Cfg::kWBytes) +
+                            16 * warp + lane / 4;
+  const uint64_t minus_magic = pack2(-12582912.f, -12582912.f);
+  uint4 w4[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+      w4[m][sub] = *reinterpret_cast<const uint4*>(codes + m * 8192 + sub * 2048);
+  uint32_t b[NBL][2][4];
+  uint64_t u[NBL];
+#pragma unroll
+  for (int j = 0; j < NBL; ++j) {
+    const int at = j * 8 * Cfg::kPitch;
+    ldsm4(b[j][0], rows + at);
+    ldsm4(b[j][1], rows + at + 64);
+    u[j] = pack2(*reinterpret_cast<const float*>(units + at),
+                 *reinterpret_cast<const float*>(units + at + Cfg::kPitch));
+  }
+  int t[2][NBL][4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint4& w = w4[m][h / 2];
+      const uint32_t lo = h % 2 ? w.z : w.x, hi = h % 2 ? w.w : w.y;
+      // even nibbles: column g; odd ones: column g + 8; 16 (u - 8) as int8
+      const uint32_t a0 = and_xor(lo << 4, 0xF0F0F0F0u, 0x80808080u);
+      const uint32_t a1 = and_xor(lo, 0xF0F0F0F0u, 0x80808080u);
+      const uint32_t a2 = and_xor(hi << 4, 0xF0F0F0F0u, 0x80808080u);
+      const uint32_t a3 = and_xor(hi, 0xF0F0F0F0u, 0x80808080u);
+#pragma unroll
+      for (int j = 0; j < NBL; ++j)
+        mma_s8(t[m][j], a0, a1, a2, a3, b[j][h / 2][h % 2 * 2], b[j][h / 2][h % 2 * 2 + 1],
+               h % kPer == 0, kMagicBits);
+    }
+    if (h % kPer != kPer - 1) continue;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int at = (kGroups == 1 ? 0 : h / kPer) * 256 + m * 128;
+      const float s0 = __bfloat162float(sc[at]), s1 = __bfloat162float(sc[at + 8]);
+      const uint64_t ss[2] = {pack2(s0, s0), pack2(s1, s1)};
+#pragma unroll
+      for (int j = 0; j < NBL; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t sum = add2(pack2(t[m][j][2 * i], t[m][j][2 * i + 1]), minus_magic);
+          acc[m][j][i] = fma2(mul2(sum, u[j]), ss[i], acc[m][j][i]);
+        }
     }
   }
 }
@@ -792,22 +881,45 @@ __device__ __forceinline__ void few_block(const uint8_t* stage, float (&acc)[2][
 // its sums.  False when a wait gave up.
 template <int KIND, int NBT, int NBL, bool DOWN>
 __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const uint8_t* smem,
-                                          float* strip, Ring& r, const ChunkInfo& info) {
+                                          Ring<FewCfg<KIND, NBT>::kStages>& r,
+                                          const ChunkInfo& info) {
   using Cfg = FewCfg<KIND, NBT>;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32 % kTeamWarps, lane = threadIdx.x % 32;
   const int len = info.len, n = info.n;
   // strips past the matrix's width have nothing to store
   const int c64 = (DOWN ? p.d : p.f) / 64 - info.c * (DOWN ? 4 : 2) - warp / 4;
   float* const sums = p.part + (size_t)info.sums * 256 + 16 * warp;
   float acc[2][NBL][4] = {};
+  auto landed = [&](const auto& at) {
+    return __all_sync(0xffffffffu, mbar_wait(&sh.full[at.st], at.ph, &sh.abort_flag)) != 0;
+  };
+  auto done = [&] {
+    if (lane == 0) mbar_arrive(&sh.empty[r.st]);
+    r.next();
+  };
+  [[maybe_unused]] uint64_t acc2[2][NBL][2] = {};         // codes: pairs of sums
 #pragma unroll 1
   for (int i = 0; i < len; ++i) {
-    if (i && !__all_sync(0xffffffffu, mbar_wait(&sh.full[r.st], r.ph, &sh.abort_flag)))
-      return false;
-    few_block<KIND, NBT, NBL>(smem + r.st * Cfg::kStageBytes, acc);
+    if (i && !landed(r)) return false;
+    const uint8_t* stage = smem + r.st * Cfg::kStageBytes;
+    if constexpr (KIND == 0)
+      few_block_bf16<NBT, NBL>(stage, acc);
+    else
+      few_block_codes<KIND, NBT, NBL>(stage, acc2);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[r.st]);
-    r.next(Cfg::kStages);
+    done();
+  }
+  if constexpr (KIND != 0) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < NBL; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = unpack2(acc2[m][j][i]);
+          acc[m][j][2 * i] = v.x;
+          acc[m][j][2 * i + 1] = v.y;
+        }
   }
   const int g = lane / 4, q = lane % 4;
 #pragma unroll
@@ -831,38 +943,27 @@ __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const
           __stcg(to + tok * 256 + g + 8, acc[m][j][2] + acc[m][j][3]);
         }
       }
-    } else if constexpr (NBL == 1) {
-      // a token's three columns (its digits): token 0 in lanes q = 0 and 1,
-      // token 1 in q = 1 and 2
+    } else {
+      // a token's three columns: its digits.  Column pairs P = 4 j + q: token
+      // 2 e has pair 3 e and the first of pair 3 e + 1, token 2 e + 1 the rest
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float c0 = acc[m][0][2 * i], c1 = acc[m][0][2 * i + 1];
-        const float after = __shfl_down_sync(0xffffffffu, c0, 1);
-        const float before = __shfl_up_sync(0xffffffffu, c1, 1);
-        if (q == 0) __stcg(to + g + 8 * i, after + (c1 + c0));
-        if (q == 2 && n > 1) __stcg(to + 256 + g + 8 * i, c1 + (c0 + before));
-      }
-    } else {
-      // a token's three columns: its digits; 8 tokens at a time through the
-      // warp's strip, then lane -> (column lane % 16, token 2 i + lane / 16)
+        float after[NBL], before[NBL];                    // of the next, of the previous pair
+        const int quad = lane & ~3;
 #pragma unroll
-      for (int ch = 0; ch < (NBL + 2) / 3; ++ch) {
-        __syncwarp();
-#pragma unroll
-        for (int jj = 3 * ch; jj < NBL && jj < 3 * ch + 3; ++jj) {
-          float* put = strip + g * kStripPitch + (jj - 3 * ch) * 8 + 2 * q;
-          *reinterpret_cast<float2*>(put) = make_float2(acc[m][jj][0], acc[m][jj][1]);
-          *reinterpret_cast<float2*>(put + 8 * kStripPitch) =
-              make_float2(acc[m][jj][2], acc[m][jj][3]);
+        for (int j = 0; j < NBL; ++j) {
+          after[j] = __shfl_sync(0xffffffffu, acc[m][j][2 * i], quad | ((q + 1) & 3));
+          before[j] = __shfl_sync(0xffffffffu, acc[m][j][2 * i + 1], quad | ((q + 3) & 3));
         }
-        __syncwarp();
-        const float* get = strip + (lane % 16) * kStripPitch;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 2 * i + lane / 16;
-          if (8 * ch + t < n)
-            __stcg(to + (8 * ch + t) * 256 + lane % 16,
-                   get[3 * t + 2] + (get[3 * t + 1] + get[3 * t]));
+        for (int j = 0; j < NBL; ++j) {
+          const float c0 = acc[m][j][2 * i], c1 = acc[m][j][2 * i + 1];
+          const int P = 4 * j + q, e = P / 3, kind = P - 3 * e;
+          const float next = q < 3 || j + 1 == NBL ? after[j] : after[j + 1 < NBL ? j + 1 : j];
+          const float prev = q > 0 || j == 0 ? before[j] : before[j > 0 ? j - 1 : 0];
+          const int tok = 2 * e + (kind == 2);
+          const float v = kind == 0 ? next + (c1 + c0) : c1 + (c0 + prev);
+          if (kind != 1 && tok < n) __stcg(to + tok * 256 + g + 8 * i, v);
         }
       }
     }
@@ -870,10 +971,10 @@ __device__ __forceinline__ bool few_chunk(const FewArgs& p, FewShared& sh, const
   return true;
 }
 
-// All chunks of a phase that this CTA takes.
+// All chunks of a phase that this team takes.
 template <int KIND, int NBT, bool DOWN>
 __device__ __forceinline__ bool few_phase(const FewArgs& p, FewShared& sh, const uint8_t* smem,
-                                          float* strip, Ring& r) {
+                                          Ring<FewCfg<KIND, NBT>::kStages>& r) {
   using Cfg = FewCfg<KIND, NBT>;
   constexpr int NB = DOWN ? Cfg::kColsD : Cfg::kColsG;
   constexpr int kPerToken = KIND ? 3 : (DOWN ? 2 : 1), kMid = KIND ? 3 : 4;
@@ -884,22 +985,22 @@ __device__ __forceinline__ bool few_phase(const FewArgs& p, FewShared& sh, const
     if (info.len == 0) {
       __syncwarp();
       if (threadIdx.x % 32 == 0) mbar_arrive(&sh.empty[r.st]);
-      r.next(Cfg::kStages);
+      r.next();
       return true;
     }
     const int nb = (info.n * kPerToken + 7) / 8;
     bool ok;
-    // as wide as needed: 1, 2, 4, 8 blocks (bf16), 1, 2, 3, 6, 12 (digits)
+    // as wide as needed: 1, 2, 4, 8 blocks (bf16), 1, 2, 3 (digits)
     if (nb == 1) {
-      ok = few_chunk<KIND, NBT, 1, DOWN>(p, sh, smem, strip, r, info);
+      ok = few_chunk<KIND, NBT, 1, DOWN>(p, sh, smem, r, info);
     } else if (NB == 2 || (NB > 2 && nb == 2)) {
-      ok = few_chunk<KIND, NBT, (NB < 2 ? 1 : 2), DOWN>(p, sh, smem, strip, r, info);
+      ok = few_chunk<KIND, NBT, (NB < 2 ? 1 : 2), DOWN>(p, sh, smem, r, info);
     } else if (NB == kMid || (NB > kMid && nb <= kMid)) {
-      ok = few_chunk<KIND, NBT, (NB < kMid ? 1 : kMid), DOWN>(p, sh, smem, strip, r, info);
+      ok = few_chunk<KIND, NBT, (NB < kMid ? 1 : kMid), DOWN>(p, sh, smem, r, info);
     } else if (NB == 2 * kMid || (NB > 2 * kMid && nb <= 2 * kMid)) {
-      ok = few_chunk<KIND, NBT, (NB < 2 * kMid ? 1 : 2 * kMid), DOWN>(p, sh, smem, strip, r, info);
+      ok = few_chunk<KIND, NBT, (NB < 2 * kMid ? 1 : 2 * kMid), DOWN>(p, sh, smem, r, info);
     } else {
-      ok = few_chunk<KIND, NBT, (NB > 2 * kMid ? NB : 1), DOWN>(p, sh, smem, strip, r, info);
+      ok = few_chunk<KIND, NBT, (NB > 2 * kMid ? NB : 1), DOWN>(p, sh, smem, r, info);
     }
     if (!ok) return false;
   }
@@ -1018,56 +1119,52 @@ __device__ void few_combine(const FewArgs& p, const FewShared& sh, const Phase& 
           : __ldg(reinterpret_cast<const uint2*>(p.x + out));
 }
 
-// All consumer warps of this CTA are done with a phase: its results are
-// visible, then counted.
+// All N consumer threads of this CTA are done with a phase: counted, once its
+// results are visible (the add's release covers what the barrier ordered).
+template <int N>
 __device__ __forceinline__ void few_arrive(const FewShared& sh, uint32_t* counter) {
-  __threadfence();
-  consumer_sync();
-  if (threadIdx.x == 0 && !*static_cast<const volatile int*>(&sh.abort_flag)) {
-    __threadfence();
-    atomicAdd(counter, 1u);
-  }
+  consumer_sync<N>();
+  if (threadIdx.x == 0 && !*static_cast<const volatile int*>(&sh.abort_flag)) red_release(counter);
 }
 // ... and all CTAs are.
+template <int N>
 __device__ __forceinline__ bool few_await(FewShared& sh, const uint32_t* counter) {
   if (threadIdx.x == 0) sh.ok = wait_count(counter, gridDim.x, &sh.abort_flag);
-  consumer_sync();
+  consumer_sync<N>();
   const bool ok = sh.ok;
-  consumer_sync();
+  consumer_sync<N>();
   return ok;
 }
 
 template <int KIND, int NBT>
 __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
   using Cfg = FewCfg<KIND, NBT>;
+  constexpr int N = Cfg::kWorkers, kWarps = N / 32;
   const int warp = threadIdx.x / 32;
-  float* strip = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStageBytes) +
-                 warp * 16 * kStripPitch;
-  Ring r;
-  const Phase up(sh, p.T, p.k, few_tiles(p.f, 128), few_tiles(p.d, Cfg::KB));
-  bool ok = few_phase<KIND, NBT, false>(p, sh, smem, strip, r);
+  Ring<Cfg::kStages> r(warp / kTeamWarps);
+  const Phase up = sh.phase[0], down = sh.phase[1];
+  bool ok = few_phase<KIND, NBT, false>(p, sh, smem, r);
   if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
-  few_arrive(sh, p.sync + kSyncG);
+  few_arrive<N>(sh, p.sync + kSyncG);
 
   const int rows = sh.row0[sh.A];
   if ((int)blockIdx.x < rows * up.nct) {     // (row, tile) to warps, CTA by CTA
-    ok = few_await(sh, p.sync + kSyncG) && ok;
+    ok = few_await<N>(sh, p.sync + kSyncG) && ok;
     if (ok)
-      for (int i = warp * gridDim.x + blockIdx.x; i < rows * up.nct; i += kFewWarps * gridDim.x)
+      for (int i = warp * gridDim.x + blockIdx.x; i < rows * up.nct; i += kWarps * gridDim.x)
         few_h<KIND>(p, sh, up, i / up.nct, i % up.nct);
   }
-  few_arrive(sh, p.sync + kSyncH);
+  few_arrive<N>(sh, p.sync + kSyncH);
 
-  const Phase down(sh, p.T, p.k, few_tiles(p.d, 256), few_tiles(p.f, Cfg::KB));
-  ok = ok && few_phase<KIND, NBT, true>(p, sh, smem, strip, r);
+  ok = ok && few_phase<KIND, NBT, true>(p, sh, smem, r);
   if (!ok) *static_cast<volatile int*>(&sh.abort_flag) = 1;
-  few_arrive(sh, p.sync + kSyncY);
+  few_arrive<N>(sh, p.sync + kSyncY);
 
   const int items = p.d / 32 * p.T;          // (token, 32 columns) to warps
   if ((int)blockIdx.x < items) {
-    ok = few_await(sh, p.sync + kSyncY) && ok;
+    ok = few_await<N>(sh, p.sync + kSyncY) && ok;
     if (ok)
-      for (int i = warp * gridDim.x + blockIdx.x; i < items; i += kFewWarps * gridDim.x) {
+      for (int i = warp * gridDim.x + blockIdx.x; i < items; i += kWarps * gridDim.x) {
         const int t = i / (p.d / 32);
         few_combine(p, sh, down, t, i - t * (p.d / 32));
       }
@@ -1076,7 +1173,7 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
 }
 
 template <int KIND, int NBT>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
     few_kernel(const __grid_constant__ FewArgs p, const __grid_constant__ CUtensorMap tmG,
                const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmD) {
   using Cfg = FewCfg<KIND, NBT>;
@@ -1087,10 +1184,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int tid = threadIdx.x;
   volatile int* abort_flag = &sh.abort_flag;
   if (tid == 0) {
-    for (int s = 0; s < Cfg::kStages; ++s) {
+    for (int s = 0; s < Cfg::kTeams * Cfg::kStages; ++s) {
       mbar_init(&sh.full[s], 1 + 32);        // the weights' thread, and each token lane
       mbar_init(&sh.ready[s], 1);
-      mbar_init(&sh.empty[s], kFewWarps);
+      mbar_init(&sh.empty[s], kTeamWarps);
     }
     sh.abort_flag = 0;
     sh.never = 0;
@@ -1100,10 +1197,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   // ---- R: router, top-k, tables
   if constexpr (KIND != 0) few_digits(p);
-  if ((int)blockIdx.x < p.KS * p.CG) few_router_rows<NBT>(p, smem);
-  __threadfence();
+  if ((int)blockIdx.x < p.KS * p.CG) few_router_rows<NBT, Cfg::kWorkers>(p, smem);
   __syncthreads();
-  if (tid == 0) atomicAdd(p.sync + kSyncRouter, 1u);
+  if (tid == 0) red_release(p.sync + kSyncRouter);
   if ((int)blockIdx.x < p.T) {
     if (tid == 0) sh.ok = wait_count(p.sync + kSyncRouter, gridDim.x, abort_flag);
     __syncthreads();
@@ -1118,21 +1214,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   fence_proxy_async_all();               // the router's staging becomes the ring
   __syncthreads();
   if (!sh.ok) return;
-  few_tables(p, sh);
+  few_tables<Cfg::kUnitTokens>(p, sh);
   if (sh.A == 0) {                       // a capacity of 0: every token passes through
-    for (size_t i = (size_t)blockIdx.x * kFewThreads + tid; i < (size_t)p.T * p.d;
-         i += (size_t)gridDim.x * kFewThreads)
+    for (size_t i = (size_t)blockIdx.x * Cfg::kThreads + tid; i < (size_t)p.T * p.d;
+         i += (size_t)gridDim.x * Cfg::kThreads)
       p.y[i] = p.x[i];
     return;
   }
 
+  if (tid / 32 == 0)
+    few_cut(p, sh, 0, few_tiles(p.f, 128), few_tiles(p.d, Cfg::KB), KIND != 0);
+  else if (tid / 32 == 1)
+    few_cut(p, sh, 1, few_tiles(p.d, 256), few_tiles(p.f, Cfg::KB), KIND != 0);
+  __syncthreads();
+
   // ---- G and D
-  if (tid < kWorkers) {
+  const int extra = tid / 32 - Cfg::kWorkers / 32;
+  if (extra < 0) {
     few_consumer<KIND, NBT>(p, sh, smem);
-  } else if (tid < kWorkers + 32) {
-    if (elect_one()) few_weights<KIND, NBT>(p, sh, smem, &tmG, &tmU, &tmD);
+  } else if (extra < Cfg::kTeams) {
+    if (elect_one()) few_weights<KIND, NBT>(p, sh, smem, extra, &tmG, &tmU, &tmD);
   } else {
-    few_tokens<KIND, NBT>(p, sh, smem);
+    few_tokens<KIND, NBT>(p, sh, smem, extra - Cfg::kTeams);
   }
 }
 
@@ -1207,7 +1310,7 @@ cudaError_t launch_few_t(const FewArgs& a, int grid, const CUtensorMap& g, const
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = s;
   // cooperative: the CTAs wait for one another, so all of them run or none
