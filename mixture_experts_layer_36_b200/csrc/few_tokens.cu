@@ -34,7 +34,6 @@
 #include "common.cuh"
 #include "few_tokens.cuh"
 #include "host_util.cuh"
-#include "w4.cuh"
 
 namespace moe {
 

@@ -1,16 +1,10 @@
-// The 4-bit weight format (include/moe.h, "4-bit expert weights"): scale and
-// code rules, and where the code of row k, column n lies in a packed matrix.
+// The 4-bit weight format (include/moe.h, "4-bit expert weights"): the scale and
+// code rules.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
 
 namespace moe {
-
-// running max |v| that a NaN or an infinity makes and keeps non-finite
-__device__ __forceinline__ float w4_max(float mx, float v) {
-  const float a = fabsf(v);
-  return (mx >= a || mx != mx) ? mx : a;       // a NaN `a` compares false: taken
-}
 
 // s = bf16(max / 7), 1 where that is 0.  __fdiv_rn: the bf16 maximum has 8
 // significant bits, so the fp32 quotient is never close enough to a bf16
@@ -27,19 +21,6 @@ __device__ __forceinline__ uint32_t w4_code(float v, float s) {
   const float r = rintf(__fdiv_rn(v, s));
   const int c = (fabsf(s) <= 3.4e38f) ? max(-7, min(7, static_cast<int>(r))) : 0;
   return static_cast<uint32_t>(c + 8);
-}
-
-struct W4Place {
-  size_t word;      // 32-bit word inside the matrix
-  int nibble;
-};
-__host__ __device__ __forceinline__ W4Place w4_place(int k, int n, int kt, int nt) {
-  (void)nt;
-  const size_t tile = (size_t)(n / 64) * kt + k / 64;
-  const int col = n % 16, row = k % 16;
-  const int lane = 4 * (col % 8) + (row % 8) / 2;
-  const int nib = (col / 8) + 2 * (row / 8) + 4 * (row % 2);
-  return {tile * 512 + (size_t)((n % 64) / 16) * 128 + lane * 4 + (k % 64) / 16, nib};
 }
 
 }  // namespace moe
