@@ -82,31 +82,54 @@ __global__ void __launch_bounds__(32 * kW4Warps)
 #pragma unroll
       for (int c = 0; c < 4; ++c) m[c] = __vmaxu2(m[c], x[c] & 0x7FFF7FFFu);
     }
+    // over the 16 rows: the first two steps also part the columns, so that a
+    // lane ends with two of them (2 c, 2 c + 1) and works out their scales only
+    const bool b1 = lane & 2, b2 = lane & 4;
+    uint32_t h[2];
 #pragma unroll
-    for (int o = 2; o < 32; o <<= 1)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
-    float s[8];
-    uint32_t packed[4];
+    for (int c = 0; c < 2; ++c)
+      h[c] = __vmaxu2(b1 ? m[2 + c] : m[c],
+                      __shfl_xor_sync(0xffffffffu, b1 ? m[c] : m[2 + c], 2));
+    uint32_t mx = __vmaxu2(b2 ? h[1] : h[0], __shfl_xor_sync(0xffffffffu, b2 ? h[0] : h[1], 4));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const __nv_bfloat16 sa = w4_scale(__uint_as_float(mx << 16));
+    const __nv_bfloat16 sb = w4_scale(__uint_as_float(mx & 0xFFFF0000u));
+    const float s0 = __bfloat162float(sa), s1 = __bfloat162float(sb);
+    const float i0 = __fdividef(1.0f, s0), i1 = __fdividef(1.0f, s1);
+    const bool plain = __all_sync(0xffffffffu, w4_scale_plain(s0) && w4_scale_plain(s1));
+    if (lane < 8 && g * kPer < t.blocks)
+      *reinterpret_cast<uint32_t*>(scale + (t.e * groups + t.k0 / G + g) * N + t.n0 +
+                                   8 * (lane % 2) + 4 * b1 + 2 * b2) =
+          (uint32_t)__bfloat16_as_ushort(sa) | (uint32_t)__bfloat16_as_ushort(sb) << 16;
+    float inv[8];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const __nv_bfloat16 a = w4_scale(__uint_as_float(m[c] << 16));
-      const __nv_bfloat16 b = w4_scale(__uint_as_float(m[c] & 0xFFFF0000u));
-      s[2 * c] = __bfloat162float(a);
-      s[2 * c + 1] = __bfloat162float(b);
-      packed[c] = (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+      const int from = (lane & ~6) | (c & 2) | (c & 1) << 2;
+      inv[2 * c] = __shfl_sync(0xffffffffu, i0, from);
+      inv[2 * c + 1] = __shfl_sync(0xffffffffu, i1, from);
     }
-    if (lane < 2 && g * kPer < t.blocks)
-      *reinterpret_cast<uint4*>(scale + (t.e * groups + t.k0 / G + g) * N + t.n0 + 8 * lane) =
-          make_uint4(packed[0], packed[1], packed[2], packed[3]);
 #pragma unroll
     for (int i = g * kPer; i < (g + 1) * kPer; ++i) {
       const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       uint32_t codes = 0;
+      if (plain) {
+        // sum of (kW4Bits + u) 16^column, less what the bits add up to
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        codes |= w4_code(__uint_as_float(x[c] << 16), s[2 * c]) << (8 * c);
-        codes |= w4_code(__uint_as_float(x[c] & 0xFFFF0000u), s[2 * c + 1]) << (8 * c + 4);
+        for (int c = 3; c >= 0; --c) {
+          codes = codes * 16 + w4_code_bits(__uint_as_float(x[c] & 0xFFFF0000u), inv[2 * c + 1]);
+          codes = codes * 16 + w4_code_bits(__uint_as_float(x[c] << 16), inv[2 * c]);
+        }
+        codes -= kW4Bits * 0x11111111u;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int from = (lane & ~6) | (c & 2) | (c & 1) << 2;
+          const float t0 = __shfl_sync(0xffffffffu, s0, from);
+          const float t1 = __shfl_sync(0xffffffffu, s1, from);
+          codes |= w4_code(__uint_as_float(x[c] << 16), t0) << (8 * c);
+          codes |= w4_code(__uint_as_float(x[c] & 0xFFFF0000u), t1) << (8 * c + 4);
+        }
       }
       words[i % 4] = w4_transpose(codes);
       if (i % 4 == 3 && i < t.blocks)
