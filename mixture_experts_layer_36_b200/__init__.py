@@ -21,5 +21,6 @@ def __getattr__(name):
         return importlib.import_module("." + name, __name__)
     binding = importlib.import_module(".binding", __name__)
     if hasattr(binding, name):
-        return getattr(binding, name)
+        globals()[name] = getattr(binding, name)       # found directly from now on
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -722,18 +722,37 @@ def moe_layer_forward_fp8(x, w_router, bias, wq_gate, s_gate, wq_up, s_up, wq_do
 
 # ----------------------------------------------------------------- 4-bit experts
 
-def _on_device(tensors):
-    """The one device that all the (name, tensor) pairs live on; the calls
-    below run there, whatever the current device is."""
-    dev = None
-    for name, t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return dev
+def _like(t, name, dtype, shape, device):
+    """_want, and on `device`: the calls below run there, whatever the current
+    device is.  One test for what is right, the messages for what is not: a
+    decode step's checks cost as much as its kernel otherwise."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device \
+            or not t.is_contiguous() or not t.is_cuda:
+        _want(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+class _At:
+    """The device (made current) and the stream that a call runs on: `stream`,
+    or the device's current one."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if torch.cuda.current_device() != device.index:
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        self.device = device
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
 
 
 def _w4_groups(K, group):
@@ -746,20 +765,21 @@ def moe_quantize_weights_w4(w, group=128, q=None, scale=None, stream=None):
     """bf16 weights [E,K,N] -> (4-bit codes uint8 [E, N/64, K/64, 2048],
     bf16 scales [E, ceil(K/group), N]); the layout is in include/moe.h."""
     _want(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError(f"w: expected shape [E, K, N], got {tuple(w.shape)}")
     E, K, N = w.shape
     groups = _w4_groups(K, group)
     if K % 64 or N % 64 or not (E and K and N):
         raise ValueError(f"K and N must be positive multiples of 64 and E positive, got {(E, K, N)}")
-    with torch.cuda.device(_on_device((("w", w), ("q", q), ("scale", scale)))), \
-            torch.cuda.stream(stream):
+    with _At(w.device, stream) as st:
         if q is None:
             q = torch.empty(E, N // 64, K // 64, 2048, dtype=torch.uint8, device=w.device)
         if scale is None:
             scale = torch.empty(E, groups, N, dtype=torch.bfloat16, device=w.device)
-        _want(q, "q", torch.uint8, (E, N // 64, K // 64, 2048))
-        _want(scale, "scale", torch.bfloat16, (E, groups, N))
+        _like(q, "q", torch.uint8, (E, N // 64, K // 64, 2048), w.device)
+        _like(scale, "scale", torch.bfloat16, (E, groups, N), w.device)
         _check("moe_quantize_weights_w4", _lib.moe_quantize_weights_w4(
-            _ptr(w), E, K, N, group, _ptr(q), _ptr(scale), _stream()))
+            w.data_ptr(), E, K, N, group, q.data_ptr(), scale.data_ptr(), st))
     return q, scale
 
 
@@ -770,14 +790,13 @@ def moe_dequantize_weights_w4(q, scale, group=128, w=None, stream=None):
     if q.dim() != 4 or q.shape[3] != 2048:
         raise ValueError(f"q: expected shape [E, N/64, K/64, 2048], got {tuple(q.shape)}")
     E, N, K = q.shape[0], q.shape[1] * 64, q.shape[2] * 64
-    _want(scale, "scale", torch.bfloat16, (E, _w4_groups(K, group), N))
-    with torch.cuda.device(_on_device((("q", q), ("scale", scale), ("w", w)))), \
-            torch.cuda.stream(stream):
+    _like(scale, "scale", torch.bfloat16, (E, _w4_groups(K, group), N), q.device)
+    with _At(q.device, stream) as st:
         if w is None:
             w = torch.empty(E, K, N, dtype=torch.bfloat16, device=q.device)
-        _want(w, "w", torch.bfloat16, (E, K, N))
+        _like(w, "w", torch.bfloat16, (E, K, N), q.device)
         _check("moe_dequantize_weights_w4", _lib.moe_dequantize_weights_w4(
-            _ptr(q), _ptr(scale), E, K, N, group, _ptr(w), _stream()))
+            q.data_ptr(), scale.data_ptr(), E, K, N, group, w.data_ptr(), st))
     return w
 
 
@@ -789,53 +808,64 @@ def moe_workspace_size_few(T, d, E, k, f):
 
 def _few_call(name, x, w_router, bias, experts, k, cf, f, extra, y, logits, topk_idx, topk_w,
               slot, counts, ws, stream):
-    """What the two few-token layers share: checks, buffers and the call."""
-    _want(x, "x", torch.bfloat16)
+    """What the two few-token layers share: checks, buffers and the call.
+    experts: (name, tensor, dtype, shape) of each expert tensor."""
     T, d = x.shape
-    _want(w_router, "w_router", torch.float32)
     E = w_router.shape[1]
-    _want(w_router, "w_router", torch.float32, (d, E))
-    if bias is not None:
-        _want(bias, "bias", torch.float32, (E,))
+    dev = x.device
     if T > MOE_FEW_MAX_TOKENS:
         raise ValueError(f"{name} takes at most {MOE_FEW_MAX_TOKENS} tokens, got {T}")
-    outs = (("logits", logits, torch.float32, (T, E)), ("topk_idx", topk_idx, torch.int32, (T, k)),
-            ("topk_w", topk_w, torch.float32, (T, k)), ("slot", slot, torch.int32, (T, k)),
-            ("counts", counts, torch.int32, (E,)))
-    for n, t, dt, shape in outs:
-        if t is not None:
-            _want(t, n, dt, shape)
-    dev = _on_device((("x", x), ("w_router", w_router), ("bias", bias), *experts,
-                      *((n, t) for n, t, _, _ in outs), ("y", y), ("ws", ws)))
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
+    _like(x, "x", torch.bfloat16, (T, d), dev)
+    _like(w_router, "w_router", torch.float32, (d, E), dev)
+    if bias is not None:
+        _like(bias, "bias", torch.float32, (E,), dev)
+    for n, t, dt, shape in experts:
+        _like(t, n, dt, shape, dev)
+    outs = []
+    for n, t, dt, shape in (("logits", logits, torch.float32, (T, E)),
+                            ("topk_idx", topk_idx, torch.int32, (T, k)),
+                            ("topk_w", topk_w, torch.float32, (T, k)),
+                            ("slot", slot, torch.int32, (T, k)),
+                            ("counts", counts, torch.int32, (E,))):
+        outs.append(None if t is None else _like(t, n, dt, shape, dev).data_ptr())
+    with _At(dev, stream) as st:
         if ws is None:
             ws = torch.empty(max(moe_workspace_size_few(T, d, E, k, f), 16), dtype=torch.uint8,
                              device=dev)
-        _want(ws, "ws", torch.uint8)
-        y = torch.empty_like(x) if y is None else y
-        _want(y, "y", torch.bfloat16, (T, d))
+        else:
+            _like(ws, "ws", torch.uint8, ws.shape, dev)
+        y = torch.empty_like(x) if y is None else _like(y, "y", torch.bfloat16, (T, d), dev)
         _check(name, getattr(_lib, name)(
-            _ptr(x), _ptr(w_router), _ptr(bias), *(_ptr(t) for _, t in experts), T, d, E, k, f,
-            float(cf), *extra, _ptr(y), _ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(slot),
-            _ptr(counts), _ptr(ws), ws.numel(), _stream()))
+            x.data_ptr(), w_router.data_ptr(), None if bias is None else bias.data_ptr(),
+            *(t.data_ptr() for _, t, _, _ in experts), T, d, E, k, f, float(cf), *extra,
+            y.data_ptr(), *outs, ws.data_ptr(), ws.numel(), st))
     return y, ws
+
+
+def _few_dims(x, w_router):
+    """(E, d) of a few-token call, after what its checks need to hold."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected shape [T, d], got {tuple(x.shape)}")
+    if w_router.dim() != 2:
+        raise ValueError(f"w_router: expected shape [d, E], got {tuple(w_router.shape)}")
+    return w_router.shape[1], x.shape[1]
 
 
 def moe_layer_forward_few(x, w_router, bias, w_gate, w_up, w_down, k, cf, y=None, logits=None,
                           topk_idx=None, topk_w=None, slot=None, counts=None, ws=None,
                           stream=None):
-    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens.
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one kernel.
     Arguments as moe_layer_forward_ex; returns (y, ws).  Keep ws (of
     moe_workspace_size_few bytes) for the next call in a decode loop."""
+    E, d = _few_dims(x, w_router)
     if w_gate.dim() != 3:
         raise ValueError(f"w_gate: expected shape [E, d, f], got {tuple(w_gate.shape)}")
-    E, d, f = w_gate.shape
-    _want(w_gate, "w_gate", torch.bfloat16, (w_router.shape[1], x.shape[1], f))
-    _want(w_up, "w_up", torch.bfloat16, (E, d, f))
-    _want(w_down, "w_down", torch.bfloat16, (E, f, d))
+    f = w_gate.shape[2]
+    bf = torch.bfloat16
     return _few_call("moe_layer_forward_few", x, w_router, bias,
-                     (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)), k, cf, f, (), y,
-                     logits, topk_idx, topk_w, slot, counts, ws, stream)
+                     (("w_gate", w_gate, bf, (E, d, f)), ("w_up", w_up, bf, (E, d, f)),
+                      ("w_down", w_down, bf, (E, f, d))), k, cf, f, (), y, logits, topk_idx,
+                     topk_w, slot, counts, ws, stream)
 
 
 def moe_layer_forward_few_w4(x, w_router, bias, q_gate, s_gate, q_up, s_up, q_down, s_down, k, cf,
@@ -843,21 +873,18 @@ def moe_layer_forward_few_w4(x, w_router, bias, q_gate, s_gate, q_up, s_up, q_do
                              counts=None, ws=None, stream=None):
     """moe_layer_forward_few on 4-bit experts (codes and scales from
     moe_quantize_weights_w4, one group size).  Returns (y, ws)."""
+    E, d = _few_dims(x, w_router)
     if q_gate.dim() != 4:
         raise ValueError(f"q_gate: expected shape [E, f/64, d/64, 2048], got {tuple(q_gate.shape)}")
-    E, d, f = w_router.shape[1], x.shape[1], q_gate.shape[1] * 64
+    f = q_gate.shape[1] * 64
     gd, gf = _w4_groups(d, group), _w4_groups(f, group)
-    for n, t, shape in (("q_gate", q_gate, (E, f // 64, d // 64, 2048)),
-                        ("q_up", q_up, (E, f // 64, d // 64, 2048)),
-                        ("q_down", q_down, (E, d // 64, f // 64, 2048))):
-        _want(t, n, torch.uint8, shape)
-    for n, t, shape in (("s_gate", s_gate, (E, gd, f)), ("s_up", s_up, (E, gd, f)),
-                        ("s_down", s_down, (E, gf, d))):
-        _want(t, n, torch.bfloat16, shape)
+    u8, bf = torch.uint8, torch.bfloat16
+    up, down = (E, f // 64, d // 64, 2048), (E, d // 64, f // 64, 2048)
     return _few_call("moe_layer_forward_few_w4", x, w_router, bias,
-                     (("q_gate", q_gate), ("s_gate", s_gate), ("q_up", q_up), ("s_up", s_up),
-                      ("q_down", q_down), ("s_down", s_down)), k, cf, f, (group,), y, logits,
-                     topk_idx, topk_w, slot, counts, ws, stream)
+                     (("q_gate", q_gate, u8, up), ("s_gate", s_gate, bf, (E, gd, f)),
+                      ("q_up", q_up, u8, up), ("s_up", s_up, bf, (E, gd, f)),
+                      ("q_down", q_down, u8, down), ("s_down", s_down, bf, (E, gf, d))), k, cf, f,
+                     (group,), y, logits, topk_idx, topk_w, slot, counts, ws, stream)
 
 
 def workspace_view(ws, field, T, d, E, k, f, cf):
