@@ -88,7 +88,7 @@ struct FewCfg {
                                      ? kFewMaxStages / 2 * (3 - kTeams) : kFit;   // of a team
   static constexpr int kSmemBytes = kTeams * kStages * kStageBytes + 1024;
   // the router's staging uses the same memory: x (fp64), then W rows
-  static constexpr int kXsBytes = 8 * NBT * kFewRouterRows * 8;
+  static constexpr int kXsBytes = (8 * NBT + 2) * kFewRouterRows * 8;
   static_assert(kXsBytes + kFewRouterRows * 32 * 4 < kSmemBytes - 1024, "router staging");
   static_assert(kWorkers * 8 * NBT * 8 < kSmemBytes - 1024, "router reduction");
 };
@@ -317,15 +317,15 @@ __device__ void few_cut(const FewArgs& p, FewShared& sh, int which, int nct, int
 // Partial sums of this CTA's rows and columns for all tokens, in fp64.
 template <int NBT, int kWorkers>
 __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
-  constexpr int RR = kFewRouterRows, TT = 8 * NBT;
+  constexpr int RR = kFewRouterRows, TT = 8 * NBT, TP = TT + 2;   // padded: no bank conflicts
   const int tid = threadIdx.x;
   const bool worker = tid < kWorkers;
   const int cg = blockIdx.x % p.CG, ks = blockIdx.x / p.CG;
   const int c = tid % p.CW, rg = tid / p.CW, nrg = kWorkers / p.CW;
   const int col0 = cg * p.CW, cols = min(p.CW, p.E - col0);
   const int k0 = (int)((long long)p.d * ks / p.KS), k1 = (int)((long long)p.d * (ks + 1) / p.KS);
-  double* xs = reinterpret_cast<double*>(smem);                    // [RR][TT]
-  float* wsm = reinterpret_cast<float*>(smem + TT * RR * 8);       // [RR][CW]
+  double* xs = reinterpret_cast<double*>(smem);                    // [RR][TP]
+  float* wsm = reinterpret_cast<float*>(smem + TP * RR * 8);       // [RR][CW]
   double acc[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) acc[t] = 0.0;
@@ -335,9 +335,10 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
     if (worker) {
       const float* src = p.w_router + (size_t)base * p.E + col0;
       if (p.E % 4 == 0) {
-        const int q = p.CW / 4;
-        for (int i = tid; i < len * q; i += kWorkers) {
-          const int r = i / q, v = i % q;
+        const int lg = __ffs(p.CW) - 3;                     // CW / 4 of 16 bytes a row
+#pragma unroll 4
+        for (int i = tid; i < len << lg; i += kWorkers) {
+          const int r = i >> lg, v = i - (r << lg);
           if (4 * v < cols)
             cp_async16(smem_u32(wsm + r * p.CW + 4 * v), src + (size_t)r * p.E + 4 * v);
         }
@@ -349,9 +350,9 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
       }
       // x as fp64, a row's tokens together: two a load below
       for (int r = tid; r < len; r += kWorkers) {
-#pragma unroll 4
-        for (int t = 0; t < TT; ++t)
-          xs[r * TT + t] = t < p.T ? (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]) : 0.0;
+#pragma unroll 8
+        for (int t = 0; t < p.T; ++t)
+          xs[r * TP + t] = (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]);
       }
       cp_async_wait();
     }
@@ -363,12 +364,12 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (r + i * nrg < len)
-              acc[i] = fma((double)wsm[(r + i * nrg) * p.CW + c], xs[(r + i * nrg) * TT], acc[i]);
+              acc[i] = fma((double)wsm[(r + i * nrg) * p.CW + c], xs[(r + i * nrg) * TP], acc[i]);
       } else {
 #pragma unroll 2
         for (int r = rg; r < len; r += nrg) {
           const double w = (double)wsm[r * p.CW + c];
-          const double2* x = reinterpret_cast<const double2*>(xs + r * TT);
+          const double2* x = reinterpret_cast<const double2*>(xs + r * TP);
 #pragma unroll
           for (int t = 0; t < TT / 2; ++t) {
             const double2 v = x[t];
@@ -1186,6 +1187,14 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
   if (!ok && threadIdx.x % 32 == 0) report(p.status, kDevErrWaitTimeout);
 }
 
+// Zeroes the workspace header (status word and counters).  The layer's kernel
+// is launched as its dependent and reads the router's weights while this one
+// and the launch itself pass: a memset in its place left 3 us between the two.
+__global__ void few_header_kernel(uint32_t* header, int words) {
+  grid_dep_launch();
+  for (int i = threadIdx.x; i < words; i += blockDim.x) header[i] = 0;
+}
+
 template <int KIND, int NBT>
 __global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
     few_kernel(const __grid_constant__ FewArgs p, const __grid_constant__ CUtensorMap tmG,
@@ -1212,6 +1221,7 @@ __global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
   // ---- R: router, top-k, tables
   if constexpr (KIND != 0) few_digits(p);
   if ((int)blockIdx.x < p.KS * p.CG) few_router_rows<NBT, Cfg::kWorkers>(p, smem);
+  grid_dep_wait();                       // the counters are zero from here on
   __syncthreads();
   if (tid == 0) red_release(p.sync + kSyncRouter);
   // One or two tokens are routed by every CTA for itself, which takes one wait
@@ -1338,11 +1348,13 @@ cudaError_t launch_few_t(const FewArgs& a, int grid, const CUtensorMap& g, const
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = s;
   // cooperative: the CTAs wait for one another, so all of them run or none
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a, g, u, dn);
 }
 
@@ -1401,7 +1413,8 @@ cudaError_t launch_few(FewArgs a, void* ws, cudaStream_t s, bool* map_failed) {
     *map_failed = true;
     return cudaSuccess;
   }
-  if ((err = cudaMemsetAsync(ws, 0, lay.sync, s)) != cudaSuccess) return err;
+  few_header_kernel<<<1, 320, 0, s>>>(static_cast<uint32_t*>(ws), (int)(lay.sync / 4));
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
   if (a.gate.group == 0) return launch_few_kind<0>(a, grid, g, u, dn, di, s);
   if (a.gate.group == 64) return launch_few_kind<2>(a, grid, g, u, dn, di, s);
   if (a.gate.group == 32) return launch_few_kind<3>(a, grid, g, u, dn, di, s);
