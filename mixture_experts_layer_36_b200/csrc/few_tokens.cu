@@ -349,10 +349,18 @@ __device__ void few_router_rows(const FewArgs& p, uint8_t* smem) {
         }
       }
       // x as fp64, a row's tokens together: two a load below
-      for (int r = tid; r < len; r += kWorkers) {
+      if (NBT == 1) {
+        for (int r = tid; r < len; r += kWorkers) {
 #pragma unroll 8
-        for (int t = 0; t < p.T; ++t)
-          xs[r * TP + t] = (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]);
+          for (int t = 0; t < p.T; ++t)
+            xs[r * TP + t] = (double)__bfloat162float(p.x[(size_t)t * p.d + base + r]);
+        }
+      } else {                                    // a warp for each token
+        for (int t = tid / 32; t < p.T; t += kWorkers / 32) {
+          const __nv_bfloat16* x = p.x + (size_t)t * p.d + base;
+#pragma unroll 8
+          for (int r = tid % 32; r < len; r += 32) xs[r * TP + t] = (double)__bfloat162float(x[r]);
+        }
       }
       cp_async_wait();
     }
