@@ -20,21 +20,28 @@ namespace moe {
 
 constexpr int kW4Warps = 4;           // of a block: 64 adjacent columns
 
-// Exchange bit B of the code index with lane bit LB: in a word and its
-// partner's, the codes whose index has that bit trade places.
-template <int LB, int B>
-__device__ __forceinline__ uint32_t w4_swap(uint32_t x) {
-  constexpr uint32_t kLow = B == 0 ? 0x0F0F0F0Fu : (B == 1 ? 0x00FF00FFu : 0x0000FFFFu);
-  constexpr int kShift = 4 << B;
-  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1 << LB);
-  return (threadIdx.x >> LB) & 1 ? (x & ~kLow) | ((y & ~kLow) >> kShift)
-                                 : (x & kLow) | ((y & kLow) << kShift);
-}
-// From 8 columns of row lane / 2 (columns 8 (lane % 2) ..) to the packed word of
-// lane w4_lane(), or back.
-__device__ __forceinline__ uint32_t w4_transpose(uint32_t x) {
-  return w4_swap<1, 2>(w4_swap<4, 1>(w4_swap<0, 0>(x)));
-}
+// The transposition of 8 codes: three times a bit of the code's index trades
+// places with a lane bit (index bits 0, 1, 2 with lane bits 0, 4, 1), codes whose
+// index has that bit going one way between two lanes.  Selections that depend on
+// the lane alone are made once.
+struct W4Transpose {
+  uint32_t keep, turn, bytes, halves;
+  __device__ W4Transpose() {
+    const int l = threadIdx.x % 32;
+    keep = l & 1 ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+    turn = l & 1 ? 28 : 4;
+    bytes = l & 16 ? 0x3715u : 0x6240u;
+    halves = l & 2 ? 0x3276u : 0x5410u;
+  }
+  // From 8 columns of row lane / 2 (columns 8 (lane % 2) ..) to the packed word of
+  // lane w4_lane(), or back.
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
+    x = (x & keep) | (__funnelshift_l(y, y, turn) & ~keep);
+    x = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 16), bytes);
+    return __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 2), halves);
+  }
+};
 // Where this lane's word lies in a block of 16 columns: 4 g + c.
 __device__ __forceinline__ int w4_lane() {
   const int l = threadIdx.x % 32;
@@ -59,6 +66,7 @@ __global__ void __launch_bounds__(32 * kW4Warps)
     w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K, int N, uint8_t* __restrict__ q,
                        __nv_bfloat16* __restrict__ scale) {
   const W4Tile t(K);
+  const W4Transpose transpose;
   const int lane = threadIdx.x % 32;
   const __nv_bfloat16* src = w + (t.e * K + t.k0 + lane / 2) * (size_t)N + t.n0 + 8 * (lane % 2);
   uint4 v[8];
@@ -70,44 +78,60 @@ __global__ void __launch_bounds__(32 * kW4Warps)
   uint4* out = reinterpret_cast<uint4*>(
       q + ((t.e * (N / 64) + t.n0 / 64) * (K / 64) + t.k0 / 64) * 2048 + (t.n0 % 64) * 32) +
       w4_lane();
+  constexpr int kG = 128 / G, kPer = G / 16;               // groups; blocks of one
+  // Largest magnitudes by group and column: as integers |NaN| > |inf| > |finite|.
+  uint32_t m[kG][4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[i / kPer][c] = __vmaxu2(m[i / kPer][c], x[c] & 0x7FFF7FFFu);
+  }
+  // Over the 16 rows in four steps, which also part columns and groups among the
+  // lanes, so that a lane ends with two columns (2 c, 2 c + 1) of one group.
+  const bool b1 = lane & 2, b2 = lane & 4, b3 = lane & 8, b4 = lane & 16;
+  auto part = [&](bool up, uint32_t lo, uint32_t hi, int mask) {
+    return __vmaxu2(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, mask));
+  };
+  uint32_t top[kG];
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+    top[g] = part(b2, part(b1, m[g][0], m[g][2], 2), part(b1, m[g][1], m[g][3], 2), 4);
+  uint32_t mx;
+  int group = 0;                                           // this lane's
+  if constexpr (kG == 4) {
+    mx = part(b4, part(b3, top[0], top[2], 8), part(b3, top[1], top[3], 8), 16);
+    group = 2 * b3 + b4;
+  } else if constexpr (kG == 2) {
+    mx = part(b3, top[0], top[1], 8);
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    group = b3;
+  } else {
+    mx = __vmaxu2(top[0], __shfl_xor_sync(0xffffffffu, top[0], 8));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+  }
+  const __nv_bfloat16 sa = w4_scale(__uint_as_float(mx << 16));
+  const __nv_bfloat16 sb = w4_scale(__uint_as_float(mx & 0xFFFF0000u));
+  const float s0 = __bfloat162float(sa), s1 = __bfloat162float(sb);
+  const float i0 = __fdividef(1.0f, s0), i1 = __fdividef(1.0f, s1);
+  const bool plain = __all_sync(0xffffffffu, w4_scale_plain(s0) && w4_scale_plain(s1));
+  if ((kG == 4 || !b4) && (kG >= 2 || !b3) && group * kPer < t.blocks)
+    *reinterpret_cast<uint32_t*>(scale + (t.e * groups + t.k0 / G + group) * N + t.n0 +
+                                 8 * (lane % 2) + 4 * b1 + 2 * b2) =
+        (uint32_t)__bfloat16_as_ushort(sa) | (uint32_t)__bfloat16_as_ushort(sb) << 16;
+  // the lane that holds columns 2 c, 2 c + 1 of group g (and this lane's half)
+  auto holder = [&](int g, int c) {
+    const int rest = kG == 4 ? (g & 2) << 2 | (g & 1) << 4 : (kG == 2 ? g << 3 : 0);
+    return (lane & 1) | (c & 2) | (c & 1) << 2 | rest;
+  };
   uint32_t words[4];
 #pragma unroll
-  for (int g = 0; g < 128 / G; ++g) {
-    constexpr int kPer = G / 16;                           // blocks of a group
-    // largest magnitude by column: as integers |NaN| > |inf| > |finite|
-    uint32_t m[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = g * kPer; i < (g + 1) * kPer; ++i) {
-      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m[c] = __vmaxu2(m[c], x[c] & 0x7FFF7FFFu);
-    }
-    // over the 16 rows: the first two steps also part the columns, so that a
-    // lane ends with two of them (2 c, 2 c + 1) and works out their scales only
-    const bool b1 = lane & 2, b2 = lane & 4;
-    uint32_t h[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      h[c] = __vmaxu2(b1 ? m[2 + c] : m[c],
-                      __shfl_xor_sync(0xffffffffu, b1 ? m[c] : m[2 + c], 2));
-    uint32_t mx = __vmaxu2(b2 ? h[1] : h[0], __shfl_xor_sync(0xffffffffu, b2 ? h[0] : h[1], 4));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-    const __nv_bfloat16 sa = w4_scale(__uint_as_float(mx << 16));
-    const __nv_bfloat16 sb = w4_scale(__uint_as_float(mx & 0xFFFF0000u));
-    const float s0 = __bfloat162float(sa), s1 = __bfloat162float(sb);
-    const float i0 = __fdividef(1.0f, s0), i1 = __fdividef(1.0f, s1);
-    const bool plain = __all_sync(0xffffffffu, w4_scale_plain(s0) && w4_scale_plain(s1));
-    if (lane < 8 && g * kPer < t.blocks)
-      *reinterpret_cast<uint32_t*>(scale + (t.e * groups + t.k0 / G + g) * N + t.n0 +
-                                   8 * (lane % 2) + 4 * b1 + 2 * b2) =
-          (uint32_t)__bfloat16_as_ushort(sa) | (uint32_t)__bfloat16_as_ushort(sb) << 16;
+  for (int g = 0; g < kG; ++g) {
     float inv[8];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int from = (lane & ~6) | (c & 2) | (c & 1) << 2;
-      inv[2 * c] = __shfl_sync(0xffffffffu, i0, from);
-      inv[2 * c + 1] = __shfl_sync(0xffffffffu, i1, from);
+      inv[2 * c] = __shfl_sync(0xffffffffu, i0, holder(g, c));
+      inv[2 * c + 1] = __shfl_sync(0xffffffffu, i1, holder(g, c));
     }
 #pragma unroll
     for (int i = g * kPer; i < (g + 1) * kPer; ++i) {
@@ -124,14 +148,13 @@ __global__ void __launch_bounds__(32 * kW4Warps)
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int from = (lane & ~6) | (c & 2) | (c & 1) << 2;
-          const float t0 = __shfl_sync(0xffffffffu, s0, from);
-          const float t1 = __shfl_sync(0xffffffffu, s1, from);
+          const float t0 = __shfl_sync(0xffffffffu, s0, holder(g, c));
+          const float t1 = __shfl_sync(0xffffffffu, s1, holder(g, c));
           codes |= w4_code(__uint_as_float(x[c] << 16), t0) << (8 * c);
           codes |= w4_code(__uint_as_float(x[c] & 0xFFFF0000u), t1) << (8 * c + 4);
         }
       }
-      words[i % 4] = w4_transpose(codes);
+      words[i % 4] = transpose(codes);
       if (i % 4 == 3 && i < t.blocks)
         out[(i / 4) * 128] = make_uint4(words[0], words[1], words[2], words[3]);
     }
@@ -143,6 +166,7 @@ __global__ void __launch_bounds__(32 * kW4Warps)
     w4_dequantize_kernel(const uint8_t* __restrict__ q, const __nv_bfloat16* __restrict__ scale,
                          int K, int N, __nv_bfloat16* __restrict__ w) {
   const W4Tile t(K);
+  const W4Transpose transpose;
   const int lane = threadIdx.x % 32;
   const uint4* src = reinterpret_cast<const uint4*>(
       q + ((t.e * (N / 64) + t.n0 / 64) * (K / 64) + t.k0 / 64) * 2048 + (t.n0 % 64) * 32) +
@@ -164,7 +188,7 @@ __global__ void __launch_bounds__(32 * kW4Warps)
     const uint32_t words[4] = {v[i / 4].x, v[i / 4].y, v[i / 4].z, v[i / 4].w};
     const uint4 sg = s4[i * 16 / G];
     const uint32_t s[4] = {sg.x, sg.y, sg.z, sg.w};
-    const uint32_t codes = w4_transpose(words[i % 4]);
+    const uint32_t codes = transpose(words[i % 4]);
     uint32_t o[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
