@@ -10,8 +10,10 @@ Bounds.  u = 2^-24 is half a step of fp32, 2^-8 half a step of bf16 (relative).
     sum of k <= 8 terms adds 7 u, the quotient u: relative (2 D + 20) u.
   * a product of n terms accumulated in fp32: n u sum |a b|.
   * h = silu(g) u: |silu'| <= 1.1, silu within 8 steps (exp, add, divide,
-    product: 16 u), the product u, and the split of h into two bf16 terms
-    leaves 2^-16 |h|; errors of g and u carried through.
+    product: 16 u), the product u; errors of g and u carried through.  On bf16
+    weights h enters the next product as two bf16 terms, which leaves 2^-16 |h|.
+  * On 4-bit codes x and h enter their products as fixed-point digits, in units of
+    at most 2^-21 of the largest of each 128 values: half a unit is 2^-22 of it.
   * y: the errors above carried through the down projection and the weighted
     sum of k terms (8 more roundings), then one rounding to bf16 (2^-8).
 """
@@ -68,10 +70,18 @@ def weights64(l32, idx):
     return w, (2 * D + 20) * U32 * w
 
 
-def layer64(x, experts, idx, slot, w):
+def largest_of_128(v):
+    """Each value's largest magnitude among its 128 (the last ones fewer)."""
+    out = torch.empty_like(v)
+    for i in range(0, v.shape[1], 128):
+        out[:, i:i + 128] = v[:, i:i + 128].abs().amax(1, keepdim=True)
+    return out
+
+
+def layer64(x, experts, idx, slot, w, digits=False):
     """(y, bound) in fp64.  experts: function e -> (Wg, Wu, Wd) fp64 on some
     device; idx, slot, w numpy; rows whose pairs are all dropped return x
-    itself with bound 0."""
+    itself with bound 0.  digits: on 4-bit codes."""
     T, d = x.shape
     k = idx.shape[1]
     X = x.double()
@@ -84,11 +94,13 @@ def layer64(x, experts, idx, slot, w):
         Wg, Wu, Wd = experts(e)
         r = X[[t for t, _ in pairs]]
         g, u = r @ Wg, r @ Wu
-        dg, du = (d * U32 * (r.abs() @ W.abs()) for W in (Wg, Wu))
+        dx = 2.0 ** -22 * largest_of_128(r) if digits else torch.zeros_like(r)
+        dg, du = (d * U32 * ((r.abs() + dx) @ W.abs()) + dx @ W.abs() for W in (Wg, Wu))
         f = g.shape[1]
         s = g * torch.sigmoid(g)
         h = s * u
-        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + (17 * U32 + 2.0 ** -16) * h.abs()
+        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + 17 * U32 * h.abs()
+        dh = dh + (2.0 ** -22 * largest_of_128(h.abs() + dh) if digits else 2.0 ** -16 * h.abs())
         o = h @ Wd
         do = dh @ Wd.abs() + f * U32 * ((h.abs() + dh) @ Wd.abs())
         for i, (t, j) in enumerate(pairs):

@@ -77,7 +77,7 @@ def check(p, k, cf, y, o, status):
     slot, counts = ref.slots(idx, E, ref.capacity(T, E, k, cf))
     assert np.array_equal(o["slot"].cpu().numpy(), slot)
     assert np.array_equal(o["counts"].cpu().numpy(), counts)
-    y64, bound = ref.layer64(x, experts64(p), idx, slot, w)
+    y64, bound = ref.layer64(x, experts64(p), idx, slot, w, digits=bool(p["group"]))
     err = (y.double() - y64).abs()
     fine = torch.isfinite(y64)
     assert torch.equal(fine, torch.isfinite(y))
@@ -376,3 +376,195 @@ def test_quantize_decode_prefill_together():
         # values of the size of the row's rms, taken 4 times over
         rms = ref_rows.square().mean().sqrt()
         assert float((y.double() - ref_rows).abs().max()) <= 4 * 5 * ref.U16 * float(rms)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize_over_the_whole_range(group):
+    """Codes and scales equal the 64-bit rule for magnitudes from the smallest
+    bf16 to the largest: the path without divisions, and the one with."""
+    E, K, N = 2, 448, 128
+    g = torch.Generator().manual_seed(group)
+    base = torch.randint(-133, 128, (E, -(-K // group), N), generator=g)
+    fall = torch.randint(0, 5, (E, K, N), generator=g)
+    mant = 1 + torch.randint(0, 128, (E, K, N), generator=g).double() / 128
+    sign = torch.randint(0, 2, (E, K, N), generator=g).double() * 2 - 1
+    exp = base.repeat_interleave(group, 1)[:, :K].double() - fall.double()
+    w = (sign * mant * torch.exp2(exp)).clamp(-3.38e38, 3.38e38).to(BF)
+    w[0] = torch.randn(K, N, generator=g).to(BF)          # plain tiles as well
+    q, s = moe.moe_quantize_weights_w4(w.cuda(), group)
+    codes, scales = ref.quantize64(w, group)
+    torch.cuda.synchronize()
+    assert torch.equal(s.cpu().double(), scales)
+    assert torch.equal(q.cpu(), ref.pack(codes))
+    back = moe.moe_dequantize_weights_w4(q, s, group).cpu()
+    assert torch.equal(back, ref.values64(codes, scales, group).to(BF))
+
+
+# ------------------------------------------------------------------ larger, and refusals
+@pytest.mark.parametrize("group", [0, 32, 128], ids=["bf16", "g32", "g128"])
+@pytest.mark.parametrize("case", [(2, 7168, 4, 2, 2048, 0.0, False),
+                                  (9, 1024, 40, 8, 1408, 1.25, True),
+                                  (32, 2048, 6, 2, 1408, 0.0, False)],
+                         ids=lambda c: "T%d-d%d-E%d-k%d-f%d" % c[:5])
+def test_layer_at_full_widths(case, group):
+    """Units cut in several chunks, many column tiles, experts of several units."""
+    T, d, E, k, f, cf, bias = case
+    p = make(T, d, E, k, f, seed=T + d, group=group, bias=bias)
+    o = outputs(T, E, k)
+    y, ws = call(p, k, cf, **o)
+    torch.cuda.synchronize()
+    check(p, k, cf, y, o, int(ws[:4].view(I32).item()))
+
+
+@pytest.mark.parametrize("group", [0, 32, 128], ids=["bf16", "g32", "g128"])
+@pytest.mark.parametrize("zeroed", [False, True], ids=["weighed", "unweighed"])
+def test_tokens_with_one_very_large_value(group, zeroed):
+    """One feature 2^14 times the others, as some models have; also where its
+    weights are zero, so that only the others make the result."""
+    T, d, E, k, f = 5, 320, 3, 2, 256
+    p = make(T, d, E, k, f, seed=14, group=0)
+    p["x"][:, 133] = 2.0 ** 14
+    p["w_router"][133] = 0
+    if zeroed:
+        for w in p["w"][:2]:
+            w[:, 133] = 0
+    if group:
+        p["group"], p["q"] = group, [moe.moe_quantize_weights_w4(w, group) for w in p["w"]]
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
+@pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
+def test_weights_past_32_bit_offsets(group):
+    """Experts that begin beyond 2^31 elements (and 2^32 bytes) of their tensor:
+    the same result as with those experts alone."""
+    d = f = 4096
+    E, k, T = 140, 2, 3                                   # 2.3 G weights a matrix
+    g = torch.Generator().manual_seed(13)
+    x = torch.randn(T, d, generator=g).to(BF).cuda()
+    last = [(torch.randn(k, d, f, generator=g) * d ** -0.5).to(BF).cuda() for _ in range(3)]
+    wr = torch.zeros(d, E, device="cuda")
+    wr[:, E - k:] = (torch.randn(d, k, generator=g) * d ** -0.5).cuda()
+    bias = torch.full((E,), -1000.0, device="cuda")
+    bias[E - k:] = 0
+    small = {"x": x, "w_router": wr[:, E - k:].contiguous(), "bias": None, "group": group,
+             "w": last}
+    big = dict(small, w_router=wr, bias=bias)
+    if group:
+        small["q"] = [moe.moe_quantize_weights_w4(w, group) for w in last]
+        big["q"] = []
+        for q, s in small["q"]:
+            Q = torch.zeros(E, *q.shape[1:], dtype=torch.uint8, device="cuda")
+            S = torch.zeros(E, *s.shape[1:], dtype=BF, device="cuda")
+            Q[E - k:], S[E - k:] = q, s
+            big["q"].append((Q, S))
+    else:
+        big["w"] = []
+        for w in last:
+            W = torch.zeros(E, d, f, dtype=BF, device="cuda")
+            W[E - k:] = w
+            big["w"].append(W)
+    o, ob = outputs(T, k, k), outputs(T, E, k)
+    y, _ = call(small, k, 0.0, **o)
+    yb, ws = call(big, k, 0.0, **ob)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(I32).item()) == 0
+    assert torch.equal(ob["topk_idx"] - (E - k), o["topk_idx"])
+    # the gate weights may differ in the last bit (another split of the router)
+    assert bool(((y.double() - yb.double()).abs() <= 2.02 * ref.U16 * y.double().abs() + 1e-30).all())
+    if not group:
+        q, s = moe.moe_quantize_weights_w4(big["w"][0], 128)
+        back = moe.moe_dequantize_weights_w4(q, s, 128)
+        q1, s1 = moe.moe_quantize_weights_w4(last[0], 128)
+        assert torch.equal(q[E - k:], q1) and torch.equal(s[E - k:], s1)
+        assert torch.equal(back[E - k:], moe.moe_dequantize_weights_w4(q1, s1, 128))
+
+
+def test_no_tokens():
+    p = make(1, 64, 4, 2, 64, seed=1, group=32)
+    p["x"] = torch.empty(0, 64, dtype=BF, device="cuda")
+    assert call(p, 2, 0.0)[0].shape == (0, 64)
+    assert call(dict(p, group=0), 2, 1.0)[0].shape == (0, 64)
+
+
+def test_binding_refusals():
+    T, d, E, k, f = 4, 128, 8, 2, 64
+    p = make(T, d, E, k, f, seed=1, group=64)
+    b = dict(p, group=0)
+    flat = [t for qs in p["q"] for t in qs]
+
+    def few(**kw):
+        a = {**b, **kw}
+        return moe.moe_layer_forward_few(a["x"], a["w_router"], a["bias"], *a["w"], a.get("k", k),
+                                         a.get("cf", 0.0), **a.get("out", {}))
+
+    def w4(i=None, t=None, **kw):
+        fl = list(flat)
+        if i is not None:
+            fl[i] = t
+        return moe.moe_layer_forward_few_w4(p["x"], p["w_router"], None, *fl, k, 0.0,
+                                            kw.get("group", 64))
+    few()
+    w4()
+    x = p["x"]
+    with pytest.raises(ValueError, match="at most 32"):
+        few(x=torch.zeros(33, d, dtype=BF, device="cuda"))
+    with pytest.raises(TypeError):
+        few(x=x.float())
+    with pytest.raises(ValueError):
+        few(x=torch.zeros(d, T, dtype=BF, device="cuda").t())         # not contiguous
+    with pytest.raises(ValueError):
+        few(x=x[:, :64].contiguous())                                 # another width
+    with pytest.raises(ValueError):
+        few(x=x[0])
+    with pytest.raises(TypeError):
+        few(w_router=p["w_router"].double())
+    with pytest.raises(ValueError):
+        few(w_router=p["w_router"].cpu())
+    with pytest.raises(ValueError):
+        few(bias=torch.zeros(E + 1, device="cuda"))
+    for i in range(3):
+        ws = list(p["w"])
+        ws[i] = ws[i][:-1].contiguous()
+        with pytest.raises(ValueError):
+            few(w=ws)
+        ws[i] = p["w"][i].cpu()
+        with pytest.raises(ValueError):
+            few(w=ws)
+    for name, t in outputs(T, E, k).items():
+        with pytest.raises(ValueError):
+            few(out={name: t[:-1].contiguous()})
+        with pytest.raises(TypeError):
+            few(out={name: t.double()})
+    with pytest.raises(ValueError):
+        few(out={"y": torch.empty(T + 1, d, dtype=BF, device="cuda")})
+    need = moe.moe_workspace_size_few(T, d, E, k, f)
+    with pytest.raises(moe.MoEError, match="WORKSPACE"):
+        few(out={"ws": torch.empty(need - 1, dtype=torch.uint8, device="cuda")})
+    with pytest.raises(moe.MoEError, match="INVALID"):
+        few(out={"ws": torch.empty(need + 16, dtype=torch.uint8, device="cuda")[1:]})
+    for kw in ({"k": 0}, {"k": 9}, {"cf": -1.0}, {"cf": math.nan}):
+        with pytest.raises((moe.MoEError, ValueError)):
+            few(**kw)
+    for i, t in enumerate(flat):
+        with pytest.raises(ValueError):
+            w4(i, t[:-1].contiguous())
+        with pytest.raises(TypeError):
+            w4(i, t.float())
+    for group in (0, 16, 32, 128, 256):                               # not the scales' one
+        with pytest.raises(ValueError):
+            w4(group=group)
+    with pytest.raises(TypeError):
+        moe.moe_quantize_weights_w4(p["w"][0].float())
+    with pytest.raises(ValueError):
+        moe.moe_quantize_weights_w4(p["w"][0], 48)
+    with pytest.raises(ValueError):
+        moe.moe_quantize_weights_w4(torch.zeros(2, 96, 64, dtype=BF, device="cuda"))
+    with pytest.raises(ValueError):
+        moe.moe_quantize_weights_w4(p["w"][0].transpose(1, 2))
+    with pytest.raises(ValueError):
+        moe.moe_dequantize_weights_w4(flat[0], flat[1], 32)
+    with pytest.raises(ValueError):
+        moe.moe_dequantize_weights_w4(flat[0][..., :1024], flat[1], 64)
