@@ -482,14 +482,21 @@ int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, in
                               int64_t N, int64_t group, void* w, void* stream);
 
 /* ---- The layer for a few tokens (a decode step) ----
- * The whole layer for up to MOE_FEW_MAX_TOKENS tokens.  Same arguments as moe_layer_forward_ex and the
- * same result, with two differences in rounding: the logits are accumulated
- * in fp64 and rounded once, and h is not rounded to bf16; a token's terms are
- * added in j order as there.  Results are bit-reproducible from run to run.  T >
- * MOE_FEW_MAX_TOKENS, d or f not a multiple of 64: MOE_ERR_UNSUPPORTED.  x,
- * w_router, the expert weights, y and ws 16-byte aligned.  The int32 at the
- * start of ws is the device status word.  Two calls that may run at the same
- * time (two streams, two graphs) need a workspace each. */
+ * The whole layer for up to MOE_FEW_MAX_TOKENS tokens in one cooperative kernel
+ * (behind a small one that zeroes its counters): the router, top-k, gate/up, down
+ * and combine, with the experts' weights as one stream through all SMs.  Same
+ * arguments as moe_layer_forward_ex and the same result but for roundings: the
+ * logits are accumulated in fp64 and rounded once (the selection is taken on
+ * these fp32 values, as there), and h is not rounded to bf16 (it enters the down
+ * projection as two bf16 terms: 2^-16).  All sums are taken in an order that the
+ * shapes, the routing and the device's SM count fix, so results are the same bits
+ * from call to call.  T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64:
+ * MOE_ERR_UNSUPPORTED.  x, w_router, the expert weights, y and ws 16-byte
+ * aligned.  The int32 at the start of ws is the device status word; nothing else
+ * in ws needs a value before a call or keeps one after it.  Two calls that may
+ * run at the same time (two streams) need a workspace each; such calls run one
+ * after the other where both want all SMs.  All pointers belong to the device
+ * that is current at the call. */
 #define MOE_FEW_MAX_TOKENS 32
 
 /* Device workspace bytes of the two calls below (0 on invalid shapes). */
@@ -504,8 +511,11 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
 
 /* moe_layer_forward_few on 4-bit experts: codes q_* and scales s_* from
  * moe_quantize_weights_w4 (gate and up: K = d, N = f; down: K = f, N = d), all
- * with the same `group`.  The products are taken on the codes, exact in bf16,
- * and each group's fp32 sum is multiplied by its scale. */
+ * with the same `group`.  The products are taken in integers: x and h enter them
+ * as fixed point with 22 bits below the largest of each 128 values of a token
+ * (exact for a bf16 x down to 2^-15 of that value, within 2^-22 of it below), and
+ * each group's exact sum is multiplied by its scale in fp32.  A longer batch
+ * takes moe_dequantize_weights_w4 and the layers above. */
 int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
                              const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,
                              const void* s_up, const uint8_t* q_down, const void* s_down,
