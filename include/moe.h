@@ -493,7 +493,8 @@ int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, in
  * from call to call.  T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64:
  * MOE_ERR_UNSUPPORTED.  x, w_router, the expert weights, y and ws 16-byte
  * aligned.  The int32 at the start of ws is the device status word; nothing else
- * in ws needs a value before a call or keeps one after it.  Two calls that may
+ * in ws needs a value before a call or keeps one after it.  y may be x (the step
+ * in place); no other output may overlap an input.  Two calls that may
  * run at the same time (two streams) need a workspace each; such calls run one
  * after the other where both want all SMs.  All pointers belong to the device
  * that is current at the call. */
@@ -513,8 +514,9 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
  * moe_quantize_weights_w4 (gate and up: K = d, N = f; down: K = f, N = d), all
  * with the same `group`.  The products are taken in integers: x and h enter them
  * as fixed point with 22 bits below the largest of each 128 values of a token
- * (exact for a bf16 x down to 2^-15 of that value, within 2^-22 of it below), and
- * each group's exact sum is multiplied by its scale in fp32.  A longer batch
+ * (exact for a bf16 x down to 2^-15 of that value, within 2^-22 of it below;
+ * values under 2^-100 as if the largest were that), and each group's exact sum is
+ * multiplied by its scale in fp32.  A longer batch
  * takes moe_dequantize_weights_w4 and the layers above. */
 int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
                              const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,

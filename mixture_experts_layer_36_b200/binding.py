@@ -738,6 +738,8 @@ class _At:
     or the device's current one."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         self.guards = []
         if torch.cuda.current_device() != device.index:
             self.guards.append(torch.cuda.device(device))

@@ -1,6 +1,7 @@
 """The few-token layer and the 4-bit weights without a GPU: refusals of the C
 entry points and of the binding, workspace sizes, and the packed layout."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -114,3 +115,9 @@ def test_binding_refusals_on_cpu_tensors():
     with pytest.raises(ValueError):
         moe.moe_dequantize_weights_w4(torch.zeros(4, 1, 1, 2048, dtype=torch.uint8),
                                       torch.zeros(4, 1, 64, dtype=bf))
+
+
+def test_a_stream_of_another_device_is_refused():
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        binding._At(torch.device("cuda", 0), other)

@@ -265,6 +265,16 @@ def test_streams_and_graphs(group):
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
+@pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
+@pytest.mark.parametrize("T, cf", [(1, 0.0), (7, 0.5), (32, 0.5)])
+def test_in_place(T, cf, group):
+    """y = x, with dropped tokens that pass through: the bits of a call out of place."""
+    p = make(T, 320, 4, 2, 192, seed=T, group=group)
+    want = call(p, 2, cf)[0].clone()
+    y, _ = call(p, 2, cf, y=p["x"])
+    assert y.data_ptr() == p["x"].data_ptr() and torch.equal(y, want)
+
+
 def test_agrees_with_the_layer_call():
     """The few-token layer and moe_layer_forward on the same inputs: same
     routing results, outputs within both calls' roundings of h and y to bf16."""
