@@ -727,34 +727,29 @@ def _like(t, name, dtype, shape, device):
     device is.  One test for what is right, the messages for what is not: a
     decode step's checks cost as much as its kernel otherwise."""
     if t is None or t.dtype is not dtype or t.shape != shape or t.device != device \
-            or not t.is_contiguous() or not t.is_cuda:
+            or not t.is_contiguous():
         _want(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t
 
 
-class _At:
-    """The device (made current) and the stream that a call runs on: `stream`,
-    or the device's current one."""
+# the handle of a device's current stream: torch.cuda.current_stream without the
+# Stream object, 0.1 instead of 2.3 us of a call that takes 7 from C
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
+
+def _run_on(device, stream, call):
+    """call(handle) with `device` current, on `stream` or the device's current
+    stream; what it allocates belongs to that stream."""
+    if stream is not None:
+        if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        self.guards = []
-        if torch.cuda.current_device() != device.index:
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
-        self.device = device
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        return call(_raw_stream(device.index))
+    with torch.cuda.device(device):
+        return call(_raw_stream(device.index))
 
 
 def _w4_groups(K, group):
@@ -773,16 +768,19 @@ def moe_quantize_weights_w4(w, group=128, q=None, scale=None, stream=None):
     groups = _w4_groups(K, group)
     if K % 64 or N % 64 or not (E and K and N):
         raise ValueError(f"K and N must be positive multiples of 64 and E positive, got {(E, K, N)}")
-    with _At(w.device, stream) as st:
-        if q is None:
-            q = torch.empty(E, N // 64, K // 64, 2048, dtype=torch.uint8, device=w.device)
-        if scale is None:
-            scale = torch.empty(E, groups, N, dtype=torch.bfloat16, device=w.device)
-        _like(q, "q", torch.uint8, (E, N // 64, K // 64, 2048), w.device)
-        _like(scale, "scale", torch.bfloat16, (E, groups, N), w.device)
+    codes, scales, dev = (E, N // 64, K // 64, 2048), (E, groups, N), w.device
+    if q is not None:
+        _like(q, "q", torch.uint8, codes, dev)
+    if scale is not None:
+        _like(scale, "scale", torch.bfloat16, scales, dev)
+
+    def call(st):
+        qo = w.new_empty(codes, dtype=torch.uint8) if q is None else q
+        so = w.new_empty(scales) if scale is None else scale
         _check("moe_quantize_weights_w4", _lib.moe_quantize_weights_w4(
-            w.data_ptr(), E, K, N, group, q.data_ptr(), scale.data_ptr(), st))
-    return q, scale
+            w.data_ptr(), E, K, N, group, qo.data_ptr(), so.data_ptr(), st))
+        return qo, so
+    return _run_on(dev, stream, call)
 
 
 def moe_dequantize_weights_w4(q, scale, group=128, w=None, stream=None):
@@ -791,15 +789,18 @@ def moe_dequantize_weights_w4(q, scale, group=128, w=None, stream=None):
     _want(q, "q", torch.uint8)
     if q.dim() != 4 or q.shape[3] != 2048:
         raise ValueError(f"q: expected shape [E, N/64, K/64, 2048], got {tuple(q.shape)}")
-    E, N, K = q.shape[0], q.shape[1] * 64, q.shape[2] * 64
-    _like(scale, "scale", torch.bfloat16, (E, _w4_groups(K, group), N), q.device)
-    with _At(q.device, stream) as st:
-        if w is None:
-            w = torch.empty(E, K, N, dtype=torch.bfloat16, device=q.device)
-        _like(w, "w", torch.bfloat16, (E, K, N), q.device)
+    E, nt, kt, _ = q.shape
+    N, K, dev = nt * 64, kt * 64, q.device
+    _like(scale, "scale", torch.bfloat16, (E, _w4_groups(K, group), N), dev)
+    if w is not None:
+        _like(w, "w", torch.bfloat16, (E, K, N), dev)
+
+    def call(st):
+        out = scale.new_empty((E, K, N)) if w is None else w
         _check("moe_dequantize_weights_w4", _lib.moe_dequantize_weights_w4(
-            q.data_ptr(), scale.data_ptr(), E, K, N, group, w.data_ptr(), st))
-    return w
+            q.data_ptr(), scale.data_ptr(), E, K, N, group, out.data_ptr(), st))
+        return out
+    return _run_on(dev, stream, call)
 
 
 # ----------------------------------------------------------------- a few tokens
@@ -808,40 +809,42 @@ def moe_workspace_size_few(T, d, E, k, f):
     return int(_lib.moe_workspace_size_few(T, d, E, k, f))
 
 
-def _few_call(name, x, w_router, bias, experts, k, cf, f, extra, y, logits, topk_idx, topk_w,
+def _few_call(name, fn, x, w_router, bias, experts, k, cf, f, extra, y, logits, topk_idx, topk_w,
               slot, counts, ws, stream):
     """What the two few-token layers share: checks, buffers and the call.
     experts: (name, tensor, dtype, shape) of each expert tensor."""
     T, d = x.shape
     E = w_router.shape[1]
     dev = x.device
+    f32, i32 = torch.float32, torch.int32
+    _want(x, "x", torch.bfloat16)
     if T > MOE_FEW_MAX_TOKENS:
         raise ValueError(f"{name} takes at most {MOE_FEW_MAX_TOKENS} tokens, got {T}")
-    _like(x, "x", torch.bfloat16, (T, d), dev)
-    _like(w_router, "w_router", torch.float32, (d, E), dev)
-    if bias is not None:
-        _like(bias, "bias", torch.float32, (E,), dev)
+    _like(w_router, "w_router", f32, (d, E), dev)
     for n, t, dt, shape in experts:
         _like(t, n, dt, shape, dev)
-    outs = []
-    for n, t, dt, shape in (("logits", logits, torch.float32, (T, E)),
-                            ("topk_idx", topk_idx, torch.int32, (T, k)),
-                            ("topk_w", topk_w, torch.float32, (T, k)),
-                            ("slot", slot, torch.int32, (T, k)),
-                            ("counts", counts, torch.int32, (E,))):
-        outs.append(None if t is None else _like(t, n, dt, shape, dev).data_ptr())
-    with _At(dev, stream) as st:
-        if ws is None:
-            ws = torch.empty(max(moe_workspace_size_few(T, d, E, k, f), 16), dtype=torch.uint8,
-                             device=dev)
-        else:
-            _like(ws, "ws", torch.uint8, ws.shape, dev)
-        y = torch.empty_like(x) if y is None else _like(y, "y", torch.bfloat16, (T, d), dev)
-        _check(name, getattr(_lib, name)(
-            x.data_ptr(), w_router.data_ptr(), None if bias is None else bias.data_ptr(),
-            *(t.data_ptr() for _, t, _, _ in experts), T, d, E, k, f, float(cf), *extra,
-            y.data_ptr(), *outs, ws.data_ptr(), ws.numel(), st))
-    return y, ws
+    if y is not None:
+        _like(y, "y", torch.bfloat16, (T, d), dev)
+    if ws is not None:
+        _like(ws, "ws", torch.uint8, ws.shape, dev)
+
+    def at(t, n, dt, shape):                       # of a tensor that may be left out
+        return None if t is None else _like(t, n, dt, shape, dev).data_ptr()
+    pairs = (T, k)
+    bias_at = at(bias, "bias", f32, (E,))
+    outs = (at(logits, "logits", f32, (T, E)), at(topk_idx, "topk_idx", i32, pairs),
+            at(topk_w, "topk_w", f32, pairs), at(slot, "slot", i32, pairs),
+            at(counts, "counts", i32, (E,)))
+
+    def call(st):
+        work = ws if ws is not None else x.new_empty(
+            max(moe_workspace_size_few(T, d, E, k, f), 16), dtype=torch.uint8)
+        out = torch.empty_like(x) if y is None else y
+        _check(name, fn(
+            x.data_ptr(), w_router.data_ptr(), bias_at, *[e[1].data_ptr() for e in experts], T, d,
+            E, k, f, cf, *extra, out.data_ptr(), *outs, work.data_ptr(), work.numel(), st))
+        return out, work
+    return _run_on(dev, stream, call)
 
 
 def _few_dims(x, w_router):
@@ -864,7 +867,7 @@ def moe_layer_forward_few(x, w_router, bias, w_gate, w_up, w_down, k, cf, y=None
         raise ValueError(f"w_gate: expected shape [E, d, f], got {tuple(w_gate.shape)}")
     f = w_gate.shape[2]
     bf = torch.bfloat16
-    return _few_call("moe_layer_forward_few", x, w_router, bias,
+    return _few_call("moe_layer_forward_few", _lib.moe_layer_forward_few, x, w_router, bias,
                      (("w_gate", w_gate, bf, (E, d, f)), ("w_up", w_up, bf, (E, d, f)),
                       ("w_down", w_down, bf, (E, f, d))), k, cf, f, (), y, logits, topk_idx,
                      topk_w, slot, counts, ws, stream)
@@ -882,7 +885,7 @@ def moe_layer_forward_few_w4(x, w_router, bias, q_gate, s_gate, q_up, s_up, q_do
     gd, gf = _w4_groups(d, group), _w4_groups(f, group)
     u8, bf = torch.uint8, torch.bfloat16
     up, down = (E, f // 64, d // 64, 2048), (E, d // 64, f // 64, 2048)
-    return _few_call("moe_layer_forward_few_w4", x, w_router, bias,
+    return _few_call("moe_layer_forward_few_w4", _lib.moe_layer_forward_few_w4, x, w_router, bias,
                      (("q_gate", q_gate, u8, up), ("s_gate", s_gate, bf, (E, gd, f)),
                       ("q_up", q_up, u8, up), ("s_up", s_up, bf, (E, gd, f)),
                       ("q_down", q_down, u8, down), ("s_down", s_down, bf, (E, gf, d))), k, cf, f,

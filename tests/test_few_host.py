@@ -120,4 +120,4 @@ def test_binding_refusals_on_cpu_tensors():
 def test_a_stream_of_another_device_is_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
-        binding._At(torch.device("cuda", 0), other)
+        binding._run_on(torch.device("cuda", 0), other, None)
