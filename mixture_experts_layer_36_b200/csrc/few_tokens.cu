@@ -471,11 +471,10 @@ __device__ void few_route(const FewArgs& p, FewShared& sh, int t0, bool write) {
 #pragma unroll
     for (int i = 0; i < kFewMaxSplits; ++i)
       v[i] = i < p.KS ? __ldcg(p.rpart + ((size_t)i * p.T + t) * p.E + tid) : 0.0;
-    double s = 0.0;
+    double s[4] = {p.bias ? (double)__ldg(p.bias + tid) : 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int i = 0; i < kFewMaxSplits; ++i) s += v[i];
-    if (p.bias) s += (double)__ldg(p.bias + tid);
-    const float l = (float)s;
+    for (int i = 0; i < kFewMaxSplits; ++i) s[i % 4] += v[i];
+    const float l = (float)((s[0] + s[1]) + (s[2] + s[3]));
     sh.logit[which][tid] = l;
     if (write) p.logits[(size_t)t * p.E + tid] = l;
   }
@@ -488,7 +487,6 @@ __device__ void few_route(const FewArgs& p, FewShared& sh, int t0, bool write) {
       const int e = tid + 32 * i;
       key[i] = e < p.E ? few_order(logit[e]) : 0u;          // no number has key 0
     }
-    float v0 = 0.f, own = 0.f, sum = 0.f;
     int own_e = 0;
     for (int j = 0; j < p.k; ++j) {
       uint32_t best = 0, be = 256;
@@ -503,15 +501,13 @@ __device__ void few_route(const FewArgs& p, FewShared& sh, int t0, bool write) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (e == tid + 32u * i) key[i] = 0u;
-      const float v = logit[e];
-      if (j == 0) v0 = v;
-      const float pj = expf(v - v0);
-      sum += pj;
-      if (tid == j) {
-        own = pj;
-        own_e = (int)e;
-      }
+      if (tid == j) own_e = (int)e;
     }
+    const float v = logit[own_e], v0 = __shfl_sync(0xffffffffu, v, 0);
+    const float own = tid < p.k ? expf(v - v0) : 0.f;
+    float sum = own;                                        // lanes 0..7 hold the k
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (tid < p.k) {
       sh.pick_e[which * p.k + tid] = own_e;
       sh.pair_w[which * p.k + tid] = own / sum;
@@ -528,9 +524,7 @@ template <int kUnitTokens>
 __device__ void few_tables(const FewArgs& p, FewShared& sh, bool local) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int pairs = p.T * p.k;
-  if (tid < 256) sh.mask[tid] = 0;
   int e = 0, t = 0;
-  __syncthreads();
   if (tid < pairs) {
     if (local) {
       e = sh.pick_e[tid];
@@ -589,7 +583,6 @@ __device__ void few_tables(const FewArgs& p, FewShared& sh, bool local) {
     }
     if (blockIdx.x == 0) p.slot[tid] = kept ? slot : -1;
   }
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------- producers
@@ -1219,6 +1212,7 @@ __global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x;
   volatile int* abort_flag = &sh.abort_flag;
+  if (tid < 256) sh.mask[tid] = 0;
   if (tid == 0) {
     for (int s = 0; s < Cfg::kTeams * Cfg::kStages; ++s) {
       mbar_init(&sh.full[s], 1 + 32);        // the weights' thread, and each token lane
@@ -1262,6 +1256,12 @@ __global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
   __syncthreads();
   if (!sh.ok) return;
   few_tables<Cfg::kUnitTokens>(p, sh, local);
+  // by warps that have no pairs
+  const int extra = tid / 32 - Cfg::kWorkers / 32;
+  if (sh.A && extra >= 0 && extra < 2)
+    few_cut(p, sh, extra, few_tiles(extra ? p.d : p.f, extra ? 256 : 128),
+            few_tiles(extra ? p.f : p.d, Cfg::KB), KIND != 0);
+  __syncthreads();
   if (sh.A == 0) {                       // a capacity of 0: every token passes through
     for (size_t i = (size_t)blockIdx.x * Cfg::kThreads + tid; i < (size_t)p.T * p.d;
          i += (size_t)gridDim.x * Cfg::kThreads)
@@ -1269,14 +1269,7 @@ __global__ void __launch_bounds__(FewCfg<KIND, NBT>::kThreads, 1)
     return;
   }
 
-  if (tid / 32 == 0)
-    few_cut(p, sh, 0, few_tiles(p.f, 128), few_tiles(p.d, Cfg::KB), KIND != 0);
-  else if (tid / 32 == 1)
-    few_cut(p, sh, 1, few_tiles(p.d, 256), few_tiles(p.f, Cfg::KB), KIND != 0);
-  __syncthreads();
-
   // ---- G and D
-  const int extra = tid / 32 - Cfg::kWorkers / 32;
   if (extra < 0) {
     few_consumer<KIND, NBT>(p, sh, smem);
   } else if (extra < Cfg::kTeams) {
