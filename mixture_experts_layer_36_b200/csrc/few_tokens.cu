@@ -202,12 +202,23 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) 
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(w), "r"(m), "r"(c));
   return r;
 }
+// The weights pass through L2 as its first lines to go: what the phases hand on,
+// the tokens and the kernel's code stay (with other memory read in between, 8
+// experts of 4096 x 14336, 32 tokens, bf16: 465 -> 442 us; fine-grained, one token,
+// codes: 64.4 -> 62.6).
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                            uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
       : "memory");
 }
 
@@ -619,6 +630,7 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem, int 
   constexpr int S = Cfg::kStages;
   volatile int* abort_flag = &sh.abort_flag;
   constexpr int kAt = KIND == 0 ? 64 : 4;      // box rows: 64 of bf16, 4 KB chunks of codes
+  const uint64_t policy = policy_evict_first();
   Ring<S> r(team);
   bool ok = true;
 #pragma unroll 1
@@ -640,10 +652,10 @@ __device__ void few_weights(const FewArgs& p, FewShared& sh, uint8_t* smem, int 
         mbar_arrive_expect_tx(bar, Cfg::kWBytes);
         const int at = (info.kb0 + i) * kAt;
         if (down) {
-          tma_load_4d(stage, tmD, bar, 0, at, col, e);
+          tma_load_4d(stage, tmD, bar, 0, at, col, e, policy);
         } else {
-          tma_load_4d(stage, tmG, bar, 0, at, col, e);
-          tma_load_4d(stage + Cfg::kWBytes / 2, tmU, bar, 0, at, col, e);
+          tma_load_4d(stage, tmG, bar, 0, at, col, e, policy);
+          tma_load_4d(stage + Cfg::kWBytes / 2, tmU, bar, 0, at, col, e, policy);
         }
         r.next();
       }
