@@ -23,6 +23,12 @@
 // The cuts follow from the shapes and the routing alone and sums are added in
 // a fixed order, so results do not depend on which CTA took what.
 //
+// Measured (at the rate of a copy, 6.55 TB/s): 256 experts of 7168 x 2048, k = 8, one
+// token 123 us on bf16 (109) and 55 on codes of groups of 128 (29), 32 tokens 2028
+// (2196) and 643 (567); 8 experts of 4096 x 14336, k = 2, groups of 64, 8 tokens 133
+// (103).  What is above the bytes is some 25 us of router, tables, grid-wide waits
+// and first blocks.
+//
 // The products run on mma.sync with the weights as the 16-row operand and the
 // tokens as the 8 columns: bf16 m16n8k16 on bf16 weights, s8 m16n8k32 on codes
 // (8 clocks an SM sub-partition each).  An SM gets 23 bytes of weights a clock
