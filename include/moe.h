@@ -487,7 +487,8 @@ int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, in
  * and combine, with the experts' weights as one stream through all SMs.  Same
  * arguments as moe_layer_forward_ex and the same result but for roundings: the
  * logits are accumulated in fp64 and rounded once (the selection is taken on
- * these fp32 values, as there), and h is not rounded to bf16 (it enters the down
+ * these fp32 values, as there; a NaN ranks below every number, and a token with
+ * less than k numbers takes its lowest NaN experts after them), and h is not rounded to bf16 (it enters the down
  * projection as two bf16 terms: 2^-16).  All sums are taken in an order that the
  * shapes, the routing and the device's SM count fix, so results are the same bits
  * from call to call.  T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64:

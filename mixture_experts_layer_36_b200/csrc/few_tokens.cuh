@@ -38,10 +38,10 @@ struct FewArgs {
 };
 
 // The order of the selection as an unsigned integer: larger logit, larger key;
-// -0 equals +0; any NaN above every number (as a NaN token's experts have to
-// be some k distinct ones).
+// -0 equals +0; any NaN below every number, as a comparison never prefers it (and
+// above 0, as a NaN token's experts have to be some k distinct ones).
 __device__ __forceinline__ uint32_t few_order(float v) {
-  if (v != v) return 0xFFFFFFFFu;
+  if (v != v) return 1u;
   const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }

@@ -29,8 +29,8 @@ def capacity(T, E, k, cf):
 
 
 def order_key(v):
-    """Selection order of fp32 values: NaN first, then descending."""
-    return (0, 0.0) if np.isnan(v) else (1, -float(v))
+    """Selection order of fp32 values: descending, NaN last."""
+    return (1, 0.0) if np.isnan(v) else (0, -float(v))
 
 
 def route(logits32, k):

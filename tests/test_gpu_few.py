@@ -161,6 +161,29 @@ def test_ties_and_masked_experts(group):
 
 
 @pytest.mark.parametrize("group", [0, 32], ids=["bf16", "w4"])
+def test_logits_that_are_no_numbers(group):
+    """An expert whose logit is NaN is not chosen while k others are numbers (as
+    in moe_layer_forward); all experts masked: the first k, with NaN weights."""
+    T, d, E, k, f = 5, 128, 12, 3, 64
+    p = make(T, d, E, k, f, seed=12, group=group)
+    p["bias"] = torch.zeros(E, device="cuda")
+    p["bias"][7] = math.nan
+    o, o2 = outputs(T, E, k), outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    moe.moe_layer_forward_ex(p["x"], p["w_router"], p["bias"], *p["w"], k, 0.0, **o2)
+    torch.cuda.synchronize()
+    assert torch.equal(o["topk_idx"], o2["topk_idx"]) and bool((o["topk_idx"] != 7).all())
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+    p["bias"] = torch.full((E,), -math.inf, device="cuda")
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    assert o["topk_idx"].tolist() == [[0, 1, 2]] * T
+    assert bool(torch.isnan(o["topk_w"]).all()) and bool(torch.isnan(y).all())
+    assert int(ws[:4].view(I32).item()) == 0
+
+
+@pytest.mark.parametrize("group", [0, 32], ids=["bf16", "w4"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_a_bad_token_stays_alone(group, bad):
     """A NaN or an infinity in one token leaves every other token's bits."""
