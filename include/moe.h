@@ -140,7 +140,8 @@ int64_t moe_workspace_field_offset(int field, int64_t T, int64_t d, int64_t E, i
  *   bias     f32  [E]       nullable; added to every token's logits
  *   logits   f32  [T,E]     out: sum_i x[t,i]*w_router[i,e] + bias[e], fp32
  *   topk_idx i32  [T,k]     out: the k largest logits, descending; equal
- *                           logits rank the lower expert index first
+ *                           logits rank the lower expert index first, a NaN
+ *                           ranks below every number (-inf included)
  *   topk_w   f32  [T,k]     out: exp(l_j - l_max) / sum over the k selected
  *   ws, ws_bytes            device scratch, >= moe_route_workspace_size
  *   dev_status              nullable device status word (see conventions)
@@ -487,9 +488,10 @@ int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, in
  * and combine, with the experts' weights as one stream through all SMs.  Same
  * arguments as moe_layer_forward_ex and the same result but for roundings: the
  * logits are accumulated in fp64 and rounded once (the selection is taken on
- * these fp32 values, as there; a NaN ranks below every number, and a token with
- * less than k numbers takes its lowest NaN experts after them), and h is not rounded to bf16 (it enters the down
- * projection as two bf16 terms: 2^-16).  All sums are taken in an order that the
+ * these fp32 values by the rule of moe_route; a token or router weight with an
+ * infinity can give NaN logits there and infinite ones here), and h is not
+ * rounded to bf16 (it enters the down projection as two bf16 terms: 2^-16).
+ * All sums are taken in an order that the
  * shapes, the routing and the device's SM count fix, so results are the same bits
  * from call to call.  T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64:
  * MOE_ERR_UNSUPPORTED.  x, w_router, the expert weights, y and ws 16-byte

@@ -439,6 +439,20 @@ __host__ __device__ __forceinline__ int weight_index(const FuseArgs& fz, int b) 
 }
 
 // ---------------------------------------------------------------- misc
+// The order of a top-k selection as an unsigned integer: larger logit, larger key;
+// -0 equals +0; a NaN below every number, -inf included (and above 0, so that 0
+// can stand for "none": a token's experts have to be some k distinct ones).
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  if (v != v) return 1u;
+  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+// The logit of a key (+0 for -0).
+__device__ __forceinline__ float logit_of_key(uint32_t key) {
+  if (key == 1u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

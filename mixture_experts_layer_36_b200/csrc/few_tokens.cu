@@ -502,7 +502,7 @@ __device__ void few_route(const FewArgs& p, FewShared& sh, int t0, bool write) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = tid + 32 * i;
-      key[i] = e < p.E ? few_order(logit[e]) : 0u;          // no number has key 0
+      key[i] = e < p.E ? logit_key(logit[e]) : 0u;          // no number has key 0
     }
     int own_e = 0;
     for (int j = 0; j < p.k; ++j) {

@@ -37,15 +37,6 @@ struct FewArgs {
   int CW, CG, KS;               // router split: columns a block, column groups, row splits
 };
 
-// The order of the selection as an unsigned integer: larger logit, larger key;
-// -0 equals +0; any NaN below every number, as a comparison never prefers it (and
-// above 0, as a NaN token's experts have to be some k distinct ones).
-__device__ __forceinline__ uint32_t few_order(float v) {
-  if (v != v) return 1u;
-  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
 // silu in fp32 to within a few ulp (the fast intrinsics' 2^-21 would show next
 // to an h that is not rounded)
 __device__ __forceinline__ float few_silu(float z) { return z / (1.0f + expf(-z)); }

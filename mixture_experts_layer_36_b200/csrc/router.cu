@@ -30,7 +30,8 @@
 // row, adds the bias, writes the logits and keeps the best experts by
 // insertion in expert order (a strictly larger value moves ahead, so equal
 // values keep the lower index first: the same selection), then the same
-// softmax arithmetic.
+// softmax arithmetic.  A NaN logit ranks below every number, -inf included, in
+// both forms.
 #include "common.cuh"
 #include "host_util.cuh"
 
@@ -87,17 +88,18 @@ struct RouterShared {
   int never;
 };
 
-// Keeps the best 8 (value, expert) pairs in descending order; called in
-// increasing expert order, a value enters ahead of a kept one only if it is
-// strictly larger, so equal values stay ordered by expert index.  From the
+// Keeps the best 8 (value, expert) pairs above -inf in descending order (empty
+// slots hold -inf and expert -1); called in increasing expert order, a value
+// enters ahead of a kept one only if it is strictly larger, so equal values stay
+// ordered by expert index, and a NaN, which is not, never enters.  From the
 // slot where it enters, the kept pairs behind it shift down one place each
 // (a displaced pair stays ahead of every later pair of equal value).
 __device__ __forceinline__ void topk_insert(float (&sv)[8], int (&se)[8], float v, int e) {
-  if (se[7] >= 0 && !(v > sv[7])) return;
+  if (!(v > sv[7])) return;
   bool shifting = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (shifting || se[i] < 0 || v > sv[i]) {
+    if (shifting || v > sv[i]) {
       const float tv = sv[i];
       const int te = se[i];
       sv[i] = v;
@@ -107,6 +109,23 @@ __device__ __forceinline__ void topk_insert(float (&sv)[8], int (&se)[8], float 
       shifting = true;
     }
   }
+}
+
+// Fills the slots below k that the insertion left empty (fewer than k logits of
+// the row are above -inf): the experts at -inf in index order, then those whose
+// logit is NaN.
+__device__ __noinline__ void topk_fill(float (&sv)[8], int (&se)[8], const float* lrow, int E,
+                                       int k) {
+  int n = 0;
+  while (n < k && se[n] >= 0) ++n;
+  for (int nan = 0; nan < 2; ++nan)
+    for (int e = 0; e < E && n < k; ++e) {
+      const float v = lrow[e];
+      if (nan ? v != v : v == -INFINITY) {
+        sv[n] = v;
+        se[n++] = e;
+      }
+    }
 }
 
 // TOPK (S = 1 only): the epilogue writes logits / topk_idx / topk_w itself.
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
         int se[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          sv[j] = 0.f;
+          sv[j] = -INFINITY;
           se[j] = -1;
         }
         float* lrow = logits + (size_t)row * E;
@@ -289,6 +308,18 @@ __global__ void __launch_bounds__(kRThreads, 1)
           }
         }
         if (valid) {
+          bool full = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) full = full && (j >= k || se[j] >= 0);
+          if (!full) {
+            float fv[8];
+            int fe[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) fv[j] = sv[j], fe[j] = se[j];
+            topk_fill(fv, fe, lrow, E, k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sv[j] = fv[j], se[j] = fe[j];
+          }
           const float mx = sv[0];
           float p[8], sum = 0.f;
 #pragma unroll
@@ -383,14 +414,15 @@ __global__ void __launch_bounds__(256)
   }
   if (part != 0 || t >= T) return;
 
-  bool live[kPerLane];
+  uint32_t key[kPerLane];               // 0: no expert, or chosen
 #pragma unroll
   for (int c = 0; c < kPerLane; ++c) {
     const int e = lane + 32 * c;
-    live[c] = e < E;
-    if (live[c]) {
+    key[c] = 0u;
+    if (e < E) {
       if (bias) v[c] += bias[e];
       logits[(size_t)t * E + e] = v[c];
+      key[c] = logit_key(v[c]);
     }
   }
   float sel_v[8];
@@ -398,26 +430,20 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (j >= k) break;
-    float bv = 0.f;
-    int be = INT32_MAX;
-#pragma unroll
-    for (int c = 0; c < kPerLane; ++c) {
-      const int e = lane + 32 * c;
-      if (live[c] && (be == INT32_MAX || v[c] > bv)) { bv = v[c]; be = e; }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, off);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, off);
-      const bool take = (oe != INT32_MAX) &&
-                        (be == INT32_MAX || ov > bv || (ov == bv && oe < be));
-      if (take) { bv = ov; be = oe; }
-    }
-    sel_v[j] = bv;
-    sel_e[j] = be;
+    uint32_t best = 0u, be = 256u;
 #pragma unroll
     for (int c = 0; c < kPerLane; ++c)
-      if (lane + 32 * c == be) live[c] = false;
+      if (key[c] > best) {
+        best = key[c];
+        be = lane + 32 * c;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? be : 256u);
+    sel_v[j] = logit_of_key(top);
+    sel_e[j] = (int)e;
+#pragma unroll
+    for (int c = 0; c < kPerLane; ++c)
+      if (lane + 32u * c == e) key[c] = 0u;
   }
   if (lane == 0) {
     const float mx = sel_v[0];

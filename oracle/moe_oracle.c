@@ -103,7 +103,8 @@ void oracle_router_logits(const uint16_t* x, const float* w_router, const float*
 
 /* Step 2 on fp32 logits (the precision the routing decision is taken in).
  * Repeated selection of the largest remaining logit; a strict '>' keeps the
- * lower expert index on ties.  Output order: descending logit.  Weights:
+ * lower expert index on ties; a NaN ranks below every number (NaNs by index).
+ * Output order: descending logit.  Weights:
  * exp(l_j - l_max) / sum over the k selected, in fp64. */
 void oracle_topk(const float* logits, int64_t T, int64_t E, int64_t k,
                  int32_t* topk_idx, double* topk_w) {
@@ -115,7 +116,7 @@ void oracle_topk(const float* logits, int64_t T, int64_t E, int64_t k,
             int64_t best = -1;
             for (int64_t e = 0; e < E; ++e) {
                 if (taken[e]) continue;
-                if (best < 0 || l[e] > l[best]) best = e;
+                if (best < 0 || l[e] > l[best] || (isnan(l[best]) && !isnan(l[e]))) best = e;
             }
             taken[best] = 1;
             topk_idx[t * k + j] = (int32_t)best;
