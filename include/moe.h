@@ -519,7 +519,9 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
  * as fixed point with 22 bits below the largest of each 128 values of a token
  * (exact for a bf16 x down to 2^-15 of that value, within 2^-22 of it below;
  * values under 2^-100 as if the largest were that), and each group's exact sum is
- * multiplied by its scale in fp32.  A longer batch
+ * multiplied by its scale in fp32, with room for any finite x and h: a product is
+ * infinite only where the sum itself is out of fp32's range (a sum's roundings are
+ * 2^-24 of it or 2^-139, whichever is more).  A longer batch
  * takes moe_dequantize_weights_w4 and the layers above. */
 int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
                              const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,

@@ -54,6 +54,7 @@ constexpr int kFewRouterRows = 384;                // router rows staged at once
 constexpr int kFewMaxSplits = 32;
 constexpr int kFewMaxStages = 10;
 constexpr int kDigitBytes = 3 * 144;               // 128 values of a token as int8 digits
+constexpr float kCodesUnit = 2048.f;               // of the sums that chunks of codes leave
 
 // The chunks of a phase keep sums of at most T*k*tiles + few_part_rows(T) tile
 // rows (1 KB each): room for 2560 chunks, 8 or more a team, of 4 tokens.
@@ -852,11 +853,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // sums group by group: that arithmetic, not the products, was half of a block's
 // time before it was done two values an instruction (8 warps, one token block:
 // 430 clocks a block with groups of 128, 590 with 64, of the 720 that HBM
-// leaves).
+// leaves).  All of it is held times 2^-11 until H and Y read the sums: 128
+// products with the top digit, times its unit, reach 2^138, also where the
+// group's scale brings them back into range.  That costs nothing (the integers
+// are read as such multiples) and changes no bits but of results below 2^-115.
 template <int KIND, int NBT, int NBL>
 __device__ __forceinline__ void few_block_codes(const uint8_t* stage, uint64_t (&acc)[2][NBL][2]) {
   using Cfg = FewCfg<KIND, NBT>;
-  constexpr int kMagicBits = 0x4B400000;                // 1.5 2^23: sums start as its bits
+  constexpr int kMagicBits = 0x45C00000;                // 1.5 2^12: sums start as its bits
   constexpr int kGroups = Cfg::KB / Cfg::G, kPer = 4 / kGroups;      // groups; k32 steps of one
   constexpr int kRowsAt = Cfg::kWBytes + Cfg::kScaleBytes;
   const int warp = threadIdx.x / 32 % kTeamWarps, lane = threadIdx.x % 32;
@@ -865,7 +869,7 @@ __device__ __forceinline__ void few_block_codes(const uint8_t* stage, uint64_t (
   const uint8_t* units = stage + kRowsAt + 128 + (lane % 4) * 2 * Cfg::kPitch;
   const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(stage + Cfg::kWBytes) +
                             16 * warp + lane / 4;
-  const uint64_t minus_magic = pack2(-12582912.f, -12582912.f);
+  const uint64_t minus_magic = pack2(-6144.f, -6144.f);
   uint4 w4[2][2];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -1076,7 +1080,10 @@ __device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, in
   }
   float h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = few_silu(g[i]) * u[i];
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (KIND != 0) g[i] *= kCodesUnit, u[i] *= kCodesUnit;
+    h[i] = few_silu(g[i]) * u[i];
+  }
   if constexpr (KIND == 0) {
     if (!valid) return;
     float lo[4];
@@ -1103,6 +1110,7 @@ __device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, in
 // y of 32 columns of token t by one warp: lane -> (columns 4 (lane % 8), every
 // fourth of the chunks of the token's rows, row after row); the four lanes'
 // weighted sums are added last.
+template <int KIND>
 __device__ void few_combine(const FewArgs& p, const FewShared& sh, const Phase& ph, int t,
                             int col32) {
   constexpr int kBatch = 8;                  // loads in flight
@@ -1111,7 +1119,8 @@ __device__ void few_combine(const FewArgs& p, const FewShared& sh, const Phase& 
   const int c = col / 256;
   // lane j < k: row j of the token
   const int row = lane < p.k ? sh.pair_row[t * p.k + lane] : -1;
-  const float weight = lane < p.k ? sh.pair_w[t * p.k + lane] : 0.f;
+  const float weight =
+      lane < p.k ? sh.pair_w[t * p.k + lane] * (KIND ? kCodesUnit : 1.f) : 0.f;
   const int2 at = row >= 0 ? few_sums(sh, ph, row, c) : make_int2(0, 0);
   const bool any = __any_sync(0xffffffffu, row >= 0);
   const float* base = p.part + col % 256;
@@ -1205,7 +1214,7 @@ __device__ void few_consumer(const FewArgs& p, FewShared& sh, uint8_t* smem) {
     if (ok)
       for (int i = warp * gridDim.x + blockIdx.x; i < items; i += kWarps * gridDim.x) {
         const int t = i / (p.d / 32);
-        few_combine(p, sh, down, t, i - t * (p.d / 32));
+        few_combine<KIND>(p, sh, down, t, i - t * (p.d / 32));
       }
   }
   if (!ok && threadIdx.x % 32 == 0) report(p.status, kDevErrWaitTimeout);

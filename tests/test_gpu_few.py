@@ -469,6 +469,30 @@ def test_tokens_with_one_very_large_value(group, zeroed):
     check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
 
 
+@pytest.mark.parametrize("group", [0, 32, 64, 128], ids=["bf16", "g32", "g64", "g128"])
+@pytest.mark.parametrize("large", ["x", "h"])
+def test_activations_near_the_largest(large, group):
+    """x, or h, up to fp32's largest exponent against small weights: finite."""
+    T, d, E, k, f = 3, 128, 4, 2, 256
+    p = make(T, d, E, k, f, seed=15, group=0)
+    if large == "x":
+        p["x"] *= 2.0 ** 120
+        p["x"][:, 77] = torch.finfo(BF).max
+        p["w_router"] *= 2.0 ** -120
+        for w in p["w"][:2]:
+            w *= 2.0 ** -110
+    else:
+        p["w"][1] *= 2.0 ** 122
+        p["w"][2] *= 2.0 ** -110
+    if group:
+        p["group"], p["q"] = group, [moe.moe_quantize_weights_w4(w, group) for w in p["w"]]
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(y).all())
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
 @pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
 def test_weights_past_32_bit_offsets(group):
     """Experts that begin beyond 2^31 elements (and 2^32 bytes) of their tensor:
