@@ -1056,6 +1056,8 @@ __device__ __forceinline__ int2 few_sums(const FewShared& sh, const Phase& ph, i
   return make_int2(ph.tile_at(row0, n, c) + r - row0, n);
 }
 
+constexpr float kBf16Max = 3.38953139e38f;             // (2 - 2^-7) 2^127
+
 // h of one row in one tile of 128 columns, by one warp: lane -> columns 2 c,
 // 2 c + 1, 8 + 2 c, 9 + 2 c of 16 (the order of the digits).
 template <int KIND>
@@ -1090,11 +1092,18 @@ __device__ void few_h(const FewArgs& p, const FewShared& sh, const Phase& ph, in
     __nv_bfloat162 hi[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      hi[i] = __floats2bfloat162_rn(h[2 * i], h[2 * i + 1]);
+      // an infinite or NaN h has no second term; a finite one past the largest bf16
+      // value has that as its first
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x = h[2 * i + j];
+        f[j] = fabsf(x) < INFINITY ? fminf(fmaxf(x, -kBf16Max), kBf16Max) : x;
+      }
+      hi[i] = __floats2bfloat162_rn(f[0], f[1]);
       const float f0 = __low2float(hi[i]), f1 = __high2float(hi[i]);
-      // an infinite or NaN h has no second term
-      lo[2 * i] = fabsf(f0) <= 3.4e38f ? h[2 * i] - f0 : 0.f;
-      lo[2 * i + 1] = fabsf(f1) <= 3.4e38f ? h[2 * i + 1] - f1 : 0.f;
+      lo[2 * i] = fabsf(f0) <= kBf16Max ? h[2 * i] - f0 : 0.f;
+      lo[2 * i + 1] = fabsf(f1) <= kBf16Max ? h[2 * i + 1] - f1 : 0.f;
     }
     __nv_bfloat16* out = p.h + (size_t)(2 * row) * p.f + c * 128 + at;
     *reinterpret_cast<__nv_bfloat162*>(out) = hi[0];

@@ -493,6 +493,26 @@ def test_activations_near_the_largest(large, group):
     check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_h_between_the_largest_bf16_and_the_largest_float(sign):
+    """h = (1 - 2^-10) 2^128 is finite in fp32 and would round to infinity in bf16."""
+    T, d, E, k, f = 1, 64, 1, 1, 64
+    p = make(T, d, E, k, f, seed=16, group=0)
+    p["x"].zero_()
+    p["x"][0, :2] = 1.0
+    for w in p["w"][:2]:
+        w.zero_()
+    p["w"][0][0, 0] = 2.0 ** 64                          # g = 2^64
+    p["w"][1][0, 0] = sign * 2.0 ** 64 * 1020 / 1024     # u = 2^64 1023 / 1024
+    p["w"][1][0, 1] = sign * 2.0 ** 64 * 3 / 1024
+    p["w"][2] *= 2.0 ** -100
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(y).all())
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
 @pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
 def test_weights_past_32_bit_offsets(group):
     """Experts that begin beyond 2^31 elements (and 2^32 bytes) of their tensor:
