@@ -734,8 +734,10 @@ def _like(t, name, dtype, shape, device):
 
 
 # the handle of a device's current stream: torch.cuda.current_stream without the
-# Stream object, 0.1 instead of 2.3 us of a call that takes 7 from C
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Stream object, 0.1 instead of 2.3 us of a call that takes 7 from C (a torch
+# without that function gives the object)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run_on(device, stream, call):

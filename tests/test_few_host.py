@@ -1,6 +1,7 @@
 """The few-token layer and the 4-bit weights without a GPU: refusals of the C
 entry points and of the binding, workspace sizes, and the packed layout."""
 import ctypes
+import importlib.util
 import types
 
 import numpy as np
@@ -121,3 +122,21 @@ def test_a_stream_of_another_device_is_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         binding._run_on(torch.device("cuda", 0), other, None)
+
+
+def test_current_stream_without_the_raw_handle(monkeypatch):
+    """A torch that does not have the private function for a stream's handle."""
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    asked = []
+
+    def current_stream(index):
+        asked.append(index)
+        return types.SimpleNamespace(cuda_stream=1234)
+    monkeypatch.setattr(torch.cuda, "current_stream", current_stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    spec = importlib.util.spec_from_file_location(binding.__package__ + ".binding_again",
+                                                  binding.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._run_on(torch.device("cuda", 1), None, lambda handle: handle) == 1234
+    assert asked == [1]
