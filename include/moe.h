@@ -517,7 +517,7 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
  * moe_quantize_weights_w4 (gate and up: K = d, N = f; down: K = f, N = d), all
  * with the same `group`.  The products are taken in integers: x and h enter them
  * as fixed point with 22 bits below the largest of each 128 values of a token
- * (exact for a bf16 x down to 2^-15 of that value, within 2^-22 of it below;
+ * (exact for a bf16 x down to 2^-14 of that value, within 2^-22 of it below;
  * values under 2^-100 as if the largest were that), and each group's exact sum is
  * multiplied by its scale in fp32, with room for any finite x and h: a product is
  * infinite only where the sum itself is out of fp32's range (a sum's roundings are

@@ -236,9 +236,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // s8 m16n8k32 does twice the products of bf16 m16n8k16 in the same 8 clocks.
 // 128 values of a token are held as v = rint(x 2^(22 - e)), 2^(e-1) <= max|x| <
 // 2^e, in three balanced base-256 digits: fixed point with 23 bits and sign
-// relative to the largest of the 128, exact for a bf16 x down to 2^-15 of it.
-// Every digit is a token column of the product; sums of 128 rows stay below
-// 2^21 and are exact.
+// relative to the largest of the 128, exact for a bf16 x down to 2^-14 of it
+// (the last bit of an 8-bit significand at 2^(e-15) is the unit 2^(e-22)).
+// Every digit is a token column of the product; sums of 128 rows are at most
+// 2^21 (digit -128, code 0) and exact.
 struct DigitScale {
   float inv;        // 2^(22 - e)
   float unit;       // 2^(e - 22) / 16, NaN if the largest is not finite

@@ -140,3 +140,29 @@ def test_current_stream_without_the_raw_handle(monkeypatch):
     spec.loader.exec_module(again)
     assert again._run_on(torch.device("cuda", 1), None, lambda handle: handle) == 1234
     assert asked == [1]
+
+
+def test_digits_of_a_bf16_value():
+    """The fixed point of the layer on codes (v = rint(x 2^(22 - e)), 2^(e-1) <= largest <
+    2^e): every bf16 x down to 2^-14 of the largest is a whole number of units, at 2^-15
+    not all are, and what is rounded is off by at most 2^-22 of the largest."""
+    sig = 1 + np.arange(128) / 128                       # the significands of bf16
+    for largest in sig:                                  # e = 1
+        for low in range(0, 20):
+            x = sig * 2.0 ** -low
+            x = x[x <= largest]
+            units = x * 2.0 ** 21
+            off = np.abs(np.rint(units) - units) * 2.0 ** -21
+            assert (off <= 2.0 ** -22 * largest).all()
+            assert (off[x >= 2.0 ** -14 * largest] == 0).all()
+    x = 2.0 ** -15 * sig                                 # beside a largest value of 1
+    assert (np.rint(x * 2.0 ** 21) != x * 2.0 ** 21).any()
+    # three balanced digits, as bytes; a block's sum with codes 16 (u - 8)
+    v = np.arange(-(1 << 22), (1 << 22) + 1)
+    d0 = (v & 255).astype(np.uint8).view(np.int8).astype(np.int64)
+    d1 = ((v - d0) >> 8 & 255).astype(np.uint8).view(np.int8).astype(np.int64)
+    d2 = ((v - d0) >> 8) - d1 >> 8
+    assert (d0 + 256 * d1 + 65536 * d2 == v).all() and np.abs(d2).max() <= 65
+    assert 128 * 128 * 128 == 1 << 21                    # digit -128 by code 0, 128 rows
+    v = round((1 + 2.0 ** -6) * 2 ** 21)
+    assert ((v >> 8) & 255) == 128                       # the middle digit -128

@@ -513,6 +513,33 @@ def test_h_between_the_largest_bf16_and_the_largest_float(sign):
     check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("low", [-14, -15])
+def test_digits_of_small_values(low, group):
+    """On codes x is exact down to 2^-14 of the largest of its 128 values, and
+    within 2^-22 of that value below: a small x beside a 1 that has no weight."""
+    T, d, E, k, f = 32, 128, 1, 1, 128
+    p = make(T, d, E, k, f, seed=17, group=0)
+    p["x"].zero_()
+    p["x"][:, 0] = 1.0
+    odd = 2 * torch.arange(T, dtype=torch.float64, device="cuda") + 1
+    p["x"][:, 1] = (2.0 ** low * (1 + odd / 128)).to(BF)
+    for w, v in zip(p["w"], (7 * 2.0 ** 12, 7 * 2.0 ** 12, 7 * 2.0 ** -10)):
+        w.zero_()
+        w[0, 1] = v
+    p["w"][2][:] = 7 * 2.0 ** -10
+    p["group"], p["q"] = group, [moe.moe_quantize_weights_w4(w, group) for w in p["w"]]
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+    if low == -14:                                       # the bounds of an exact x
+        slot = o["slot"].cpu().numpy()
+        w = o["topk_w"].cpu().double().numpy()
+        y64, bound = ref.layer64(p["x"], experts64(p), o["topk_idx"].cpu().numpy(), slot, w)
+        assert bool(((y.double() - y64).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
 def test_weights_past_32_bit_offsets(group):
     """Experts that begin beyond 2^31 elements (and 2^32 bytes) of their tensor:
