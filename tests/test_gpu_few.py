@@ -540,6 +540,44 @@ def test_digits_of_small_values(low, group):
         assert bool(((y.double() - y64).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T, cf", [(1, 0.0), (9, 1.25), (32, 0.0)])
+def test_layer_takes_any_code_and_scale(T, cf, group):
+    """Codes 0..15, which the quantizer does not all make, and scales of both signs
+    and zero."""
+    d, E, k, f = 320, 5, 2, 192
+    p = make(T, d, E, k, f, seed=18, group=0)
+    g = torch.Generator().manual_seed(19)
+    p["group"], p["q"] = group, []
+    for K, N in ((d, f), (d, f), (f, d)):
+        q = torch.randint(0, 256, (E, N // 64, K // 64, 2048), generator=g, dtype=torch.uint8)
+        s = torch.randn(E, -(-K // group), N, generator=g) * K ** -0.5 / 4
+        s[:, 0, 3::7] = 0
+        p["q"].append((q.cuda(), s.to(BF).cuda()))
+    o = outputs(T, E, k)
+    y, ws = call(p, k, cf, **o)
+    torch.cuda.synchronize()
+    check(p, k, cf, y, o, int(ws[:4].view(I32).item()))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_largest_sums_of_digits(sign, group):
+    """Code 0 against digits of -128 in all rows: x = 1 + 2^-6 is 2^21 + 2^15 units,
+    whose middle digit is -128."""
+    T, d, E, k, f = 3, 256, 1, 1, 128
+    p = make(T, d, E, k, f, seed=20, group=0)
+    p["x"][:] = sign * (1 + 2.0 ** -6)
+    p["group"] = group
+    p["q"] = [(torch.zeros(E, N // 64, K // 64, 2048, dtype=torch.uint8, device="cuda"),
+               torch.full((E, -(-K // group), N), 2.0 ** -9, dtype=BF, device="cuda"))
+              for K, N in ((d, f), (d, f), (f, d))]
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
 @pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
 def test_weights_past_32_bit_offsets(group):
     """Experts that begin beyond 2^31 elements (and 2^32 bytes) of their tensor:
