@@ -449,6 +449,20 @@ def test_layer_at_full_widths(case, group):
     check(p, k, cf, y, o, int(ws[:4].view(I32).item()))
 
 
+@pytest.mark.parametrize("group", [0, 64], ids=["bf16", "w4"])
+@pytest.mark.parametrize("T, d, E", [(1, 12352, 8), (3, 15040, 7), (12, 12352, 6), (32, 15040, 8),
+                                     (2, 7168, 250), (9, 7168, 256), (32, 7168, 254)])
+def test_router_rows_of_two_passes(T, d, E, group):
+    """Wide layers, whose router rows a CTA stages in two passes of 384 and the rest
+    (d / 32 rows of 8 experts; of 225 experts and more d / 18 on 148 SMs)."""
+    k, f = 2, 64
+    p = make(T, d, E, k, f, seed=T + E, group=group, bias=E % 4 == 0)
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
 @pytest.mark.parametrize("group", [0, 32, 128], ids=["bf16", "g32", "g128"])
 @pytest.mark.parametrize("zeroed", [False, True], ids=["weighed", "unweighed"])
 def test_tokens_with_one_very_large_value(group, zeroed):
