@@ -638,6 +638,73 @@ def test_weights_past_32_bit_offsets(group):
         assert torch.equal(back[E - k:], moe.moe_dequantize_weights_w4(q1, s1, 128))
 
 
+@pytest.mark.parametrize("T, d, f, group", [(2, 1 << 20, 64, 0), (3, 64, 1 << 20, 0),
+                                            (2, 1 << 17, 64, 64), (9, 64, 1 << 17, 32)])
+def test_widest_layers(T, d, f, group):
+    """Widths up to the largest allowed."""
+    E, k = 2, 1
+    p = make(T, d, E, k, f, seed=21, group=group)
+    o = outputs(T, E, k)
+    y, ws = call(p, k, 0.0, **o)
+    torch.cuda.synchronize()
+    check(p, k, 0.0, y, o, int(ws[:4].view(I32).item()))
+
+
+def test_layers_one_after_another():
+    """Four layers of a model on one workspace, bf16 and codes in turn, each call's
+    tokens written by the kernel before it: the bits of the same calls with a
+    synchronization between, called and as a graph."""
+    T, d, E, k, f, group = 6, 256, 12, 3, 192, 64
+    layers = [make(T, d, E, k, f, seed=30 + i, group=group if i % 2 else 0, bias=True)
+              for i in range(4)]
+    ws = torch.empty(moe.moe_workspace_size_few(T, d, E, k, f), dtype=torch.uint8, device="cuda")
+    x0 = layers[0]["x"].clone()
+    bufs = [torch.empty_like(x0) for _ in range(5)]
+
+    def model(sync):
+        torch.mul(x0, 1.5, out=bufs[0])
+        for i, p in enumerate(layers):
+            call(dict(p, x=bufs[i]), k, 1.0, y=bufs[i + 1], ws=ws)
+            if sync:
+                torch.cuda.synchronize()
+            bufs[i + 1].add_(bufs[i])
+            if sync:
+                torch.cuda.synchronize()
+    model(True)
+    want = bufs[4].clone()
+    assert bool(torch.isfinite(want).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        model(False)
+    for run in (lambda: model(False), graph.replay) * 10:
+        for b in bufs:
+            b.fill_(math.nan)
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[4], want)
+
+
+@pytest.mark.parametrize("E, K, N, group", [(65535, 64, 64, 128), (1, 1 << 20, 64, 32),
+                                            (1, 64, 1 << 20, 64)])
+def test_largest_conversions(E, K, N, group):
+    """The most experts, the longest and the widest matrix: corners against the same
+    corners alone."""
+    g = torch.Generator(device="cuda").manual_seed(22)
+    w = torch.randn(E, K, N, generator=g, device="cuda", dtype=BF)
+    q, s = moe.moe_quantize_weights_w4(w, group)
+    back = moe.moe_dequantize_weights_w4(q, s, group)
+    for e in {0, E // 2, E - 1}:
+        for k0 in {0, (K - 64) // 128 * 128}:
+            for n0 in {0, N - 64}:
+                part = w[e:e + 1, k0:k0 + 64, n0:n0 + 64].contiguous()
+                codes, scales = ref.quantize64(part.cpu(), group)
+                assert torch.equal(back[e:e + 1, k0:k0 + 64, n0:n0 + 64].cpu(),
+                                   ref.values64(codes, scales, group).to(BF))
+    half = ref.U16 * w.abs().max().double()
+    step = s.abs().max().double()
+    assert float((back.double() - w.double()).abs().max()) <= float(0.52 * step + half)
+
+
 def test_no_tokens():
     p = make(1, 64, 4, 2, 64, seed=1, group=32)
     p["x"] = torch.empty(0, 64, dtype=BF, device="cuda")
