@@ -490,11 +490,10 @@ int moe_dequantize_weights_w4(const uint8_t* q, const void* scale, int64_t E, in
  * logits are accumulated in fp64 and rounded once (the selection is taken on
  * these fp32 values by the rule of moe_route; a token or router weight with an
  * infinity can give NaN logits there and infinite ones here), and h is not
- * rounded to bf16 (it enters the down projection as two bf16 terms: 2^-16).
- * All sums are taken in an order that the
- * shapes, the routing and the device's SM count fix, so results are the same bits
- * from call to call.  T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64:
- * MOE_ERR_UNSUPPORTED.  x, w_router, the expert weights, y and ws 16-byte
+ * rounded to bf16 (it enters the down projection as two bf16 terms: 2^-16).  All
+ * sums are taken in an order that the shapes, the routing and the device's SM
+ * count fix, so results are the same bits from call to call.
+ * T > MOE_FEW_MAX_TOKENS, d or f not a multiple of 64: MOE_ERR_UNSUPPORTED.  x, w_router, the expert weights, y and ws 16-byte
  * aligned.  The int32 at the start of ws is the device status word; nothing else
  * in ws needs a value before a call or keeps one after it.  y may be x (the step
  * in place); no other output may overlap an input.  Two calls that may
@@ -521,8 +520,10 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
  * values under 2^-100 as if the largest were that), and each group's exact sum is
  * multiplied by its scale in fp32, with room for any finite x and h: a product is
  * infinite only where the sum itself is out of fp32's range (a sum's roundings are
- * 2^-24 of it or 2^-139, whichever is more).  A longer batch
- * takes moe_dequantize_weights_w4 and the layers above. */
+ * 2^-24 of it or 2^-139, whichever is more).  An x or h that is not finite makes
+ * all sums of its token in that product NaN; a scale that is not finite makes its
+ * column's sums infinite or NaN.  A batch of more tokens takes several calls, or
+ * moe_dequantize_weights_w4 and the layers above. */
 int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
                              const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,
                              const void* s_up, const uint8_t* q_down, const void* s_down,

@@ -4,8 +4,8 @@
 // With T tokens and A distinct experts chosen, the layer reads 3 A d f weights
 // and takes 2 operations per weight and token: for T <= 32 the time is the
 // weights' bytes at the HBM rate, plus whatever keeps the memory idle.  So the
-// kernel is one stream of weights: one CTA per SM, each with an equal share of
-// the blocks of all matrices, a ring of shared-memory stages that a producer
+// kernel is one stream of weights: one CTA per SM, which takes chunks of the
+// matrices' blocks from a counter, a ring of shared-memory stages that a producer
 // warp fills by TMA, and the dependencies between the steps taken inside the
 // kernel (a cooperative launch), where the ring stays full across them:
 //   R  router: every CTA sums its rows of x Wr in fp64 (the choice of experts
@@ -23,11 +23,14 @@
 // The cuts follow from the shapes and the routing alone and sums are added in
 // a fixed order, so results do not depend on which CTA took what.
 //
-// Measured (at the rate of a copy, 6.55 TB/s): 256 experts of 7168 x 2048, k = 8, one
-// token 123 us on bf16 (109) and 55 on codes of groups of 128 (29), 32 tokens 2028
-// (2196) and 643 (567); 8 experts of 4096 x 14336, k = 2, groups of 64, 8 tokens 133
-// (103).  What is above the bytes is some 25 us of router, tables, grid-wide waits
-// and first blocks.
+// Measured (in brackets the bytes at the rate of a copy, 6.55 TB/s), on several
+// boxes: 256 experts of 7168 x 2048, k = 8, one token 121 to 123 us on bf16 (109) and
+// 52 to 55 on codes of groups of 128 (29), 32 tokens 2022 to 2146 (2196) and 623 to
+// 657 (567); 8 experts of 4096 x 14336, k = 2, groups of 64, 8 tokens 123 to 157 (86
+// to 114 for 6 to 8 experts chosen).  What is above the bytes is some 25 us of
+// router, tables, grid-wide waits and first blocks; on codes of few experts with
+// many tokens each also the products themselves (32 tokens 227 to 275, groups of
+// 128, of 111).
 //
 // The products run on mma.sync with the weights as the 16-row operand and the
 // tokens as the 8 columns: bf16 m16n8k16 on bf16 weights, s8 m16n8k32 on codes
@@ -47,7 +50,10 @@ namespace moe {
 // that issues the weights' copies and a warp that loads token rows, with a ring
 // of stages and a row of chunks of its own.  bf16 blocks leave one team idle
 // half the time; on codes two teams hide one another's latencies (8 warps: 480
-// clocks a block at one token block, 680 at three; 2 x 8: 330 and 630).
+// clocks a block at one token block, 680 at three; 2 x 8: 330 and 630), although
+// 640 threads leave 96 registers each and the forms on codes then spill 40 to 220
+// bytes (the bf16 ones, 320 threads of up to 168, 8 at most).  One team for
+// units of more than 8 tokens, with registers for them, is not tried.
 constexpr int kTeamWarps = 8;
 constexpr int kFewMaxPairs = MOE_FEW_MAX_TOKENS * 8;
 constexpr int kFewRouterRows = 384;                // router rows staged at once
