@@ -522,8 +522,9 @@ int moe_layer_forward_few(const void* x, const float* w_router, const float* bia
  * infinite only where the sum itself is out of fp32's range (a sum's roundings are
  * 2^-24 of it or 2^-139, whichever is more).  An x or h that is not finite makes
  * all sums of its token in that product NaN; a scale that is not finite makes its
- * column's sums infinite or NaN.  A batch of more tokens takes several calls, or
- * moe_dequantize_weights_w4 and the layers above. */
+ * column's sums infinite or NaN.  A batch of more tokens takes several calls (with
+ * cf = 0: a capacity counts one call's tokens), or moe_dequantize_weights_w4 and
+ * the layers above. */
 int moe_layer_forward_few_w4(const void* x, const float* w_router, const float* bias,
                              const uint8_t* q_gate, const void* s_gate, const uint8_t* q_up,
                              const void* s_up, const uint8_t* q_down, const void* s_down,
